@@ -50,6 +50,54 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
 cudaError_t launch_router_tc(const void* x, const void* wr, int T, int H, int E, float* logits, int* err,
                              cudaStream_t st);
 
+// select.cu: experts and weights of a routing rule
+struct SelectArgs {
+    const float* logits;    // [T, E], rows ld apart
+    const float* bias;      // [E] or null
+    int32_t* ids;           // [T, k]
+    float* w;               // [T, k]
+    long long ld;
+    int T, E, k;
+    int G, per, keep;       // groups of `per` experts, groups that stay
+    bool sigmoid, top2, renorm;
+    float scale;
+};
+cudaError_t launch_select(const SelectArgs& a, cudaStream_t st);
+
+// adapters.cu
+constexpr int kAdapterMaxRank = 128;
+struct AdapterArgs {
+    const void* x;          // bf16 [T, K]
+    const void* y;          // bf16 or fp32 [T, N]
+    void* out;              // as y; may be y
+    const int32_t* ids;     // [T]
+    const void* a;          // bf16 [n, R, K]
+    const void* b;          // bf16 [n, N, R]
+    const float* scales;    // [n]
+    const int32_t* ranks;   // [n] or null
+    long long ld_x, ld_y, ld_out;
+    int T, K, N, R, n;
+    bool wide;              // y and out are fp32
+};
+cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st);
+
+// block_norm.cu
+enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateElement = 3 };
+struct NormArgs {
+    const void* r;          // bf16 or fp32 [T, H]
+    const void* y;          // bf16 [T, H] or null
+    const void* w_post;     // bf16 [H] or null
+    const void* gate;       // bf16 [H], fp32 [T] or bf16 [T, H] by gate_kind
+    const void* w_pre;      // bf16 [H] (with x_out)
+    void* r_out;            // as r, or null; may be r
+    void* x_out;            // bf16 [T, H] or null; may be y
+    long long ld_r, ld_y, ld_gate, ld_r_out, ld_x;
+    int T, H, gate_kind;
+    bool r_fp32, gate_sigmoid;
+    float eps, branch_scale, residual_scale, offset;
+};
+cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t st);
+
 // moe_api.cu: text returned by moe_last_error(NULL) on this host thread
 void set_thread_error(const char* msg);
 

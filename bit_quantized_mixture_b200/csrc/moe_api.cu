@@ -1,6 +1,8 @@
 // C ABI of the routed-expert MoE layer: handle, arena, workspace, argument
 // validation and dispatch to the kernels.  Declarations and the contract of
 // every entry point are in include/moe_b200.h.
+#include <float.h>
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -62,6 +64,10 @@ struct moe_layer {
     float *w_perm = nullptr, *ts_perm = nullptr;
     __half *o = nullptr, *o_sh = nullptr;
     float* tok_scale = nullptr;
+    // moe_set_routing: the rule that the route calls follow, its bias [E]
+    bool rule_set = false;
+    moe_routing rule{};
+    float* rule_bias = nullptr;
     // state
     bool router_loaded = false;
     bool shared_loaded = false;
@@ -226,6 +232,7 @@ moe_status moe_create(const moe_config* cfg, moe_handle* out) {
     const size_t o_err = carve(sizeof(int));
     const size_t o_table = carve(sizeof(void*) * (size_t)E);
     const size_t o_gtab = carve(sizeof(float) * 2 * (size_t)E);
+    const size_t o_rbias = carve(sizeof(float) * (size_t)E);
     const size_t o_xq = carve(Tm * H * 2);
     const size_t o_tsc = carve(Tm * sizeof(float));
     const size_t o_xp = carve(slots * H * 2);
@@ -264,6 +271,7 @@ moe_status moe_create(const moe_config* cfg, moe_handle* out) {
     h->dev_err = reinterpret_cast<int*>(h->ws + o_err);
     h->table = reinterpret_cast<const uint8_t**>(h->ws + o_table);
     h->g_tab = reinterpret_cast<float*>(h->ws + o_gtab);
+    h->rule_bias = reinterpret_cast<float*>(h->ws + o_rbias);
     h->xq = reinterpret_cast<__nv_bfloat16*>(h->ws + o_xq);
     h->tok_scale = reinterpret_cast<float*>(h->ws + o_tsc);
     h->xp = reinterpret_cast<__nv_bfloat16*>(h->ws + o_xp);
@@ -426,6 +434,25 @@ static moe_status check_tokens(moe_layer* h, const char* fn, int32_t T) {
     return MOE_OK;
 }
 
+static SelectArgs select_args(const float* logits, int64_t ld, int32_t T, int32_t E, int32_t k, const moe_routing& r,
+                              const float* bias, int32_t* ids, float* w) {
+    SelectArgs a{};
+    a.logits = logits; a.bias = bias; a.ids = ids; a.w = w; a.ld = ld;
+    a.T = T; a.E = E; a.k = k;
+    a.G = r.num_groups; a.per = E / r.num_groups; a.keep = r.top_groups;
+    a.sigmoid = r.score == MOE_SCORE_SIGMOID;
+    a.top2 = r.group_score == MOE_GROUP_TOP2;
+    a.renorm = r.renorm != 0;
+    a.scale = r.scale;
+    return a;
+}
+
+// selection by the handle's rule (moe_set_routing)
+static SelectArgs handle_select_args(moe_layer* h, const float* logits, int32_t T, int32_t* ids, float* w) {
+    return select_args(logits, h->cfg.num_experts, T, h->cfg.num_experts, h->cfg.top_k, h->rule,
+                       h->rule.bias ? h->rule_bias : nullptr, ids, w);
+}
+
 moe_status moe_route(moe_handle h, const void* x, int32_t T, int32_t* topk_ids, float* topk_w, float* logits_out,
                      moe_stream_t stream) {
     if (!h) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_route: null handle");
@@ -441,7 +468,7 @@ moe_status moe_route(moe_handle h, const void* x, int32_t T, int32_t* topk_ids, 
     a.wr = h->router;
     a.logits_in = nullptr;
     a.logits = logits_out ? logits_out : h->logits;
-    a.ids = topk_ids;
+    a.ids = h->rule_set ? nullptr : topk_ids;      // with a rule: logits here, the selection below
     a.w = topk_w;
     a.counter = h->route_counter;
     a.err = h->dev_err;
@@ -449,6 +476,8 @@ moe_status moe_route(moe_handle h, const void* x, int32_t T, int32_t* topk_ids, 
     cudaStream_t st = (cudaStream_t)stream;
     if (h->prof[0]) cudaEventRecord(h->prof[0], st);
     cudaError_t e = launch_route(a, st);
+    if (e == cudaSuccess && h->rule_set && topk_ids)
+        e = launch_select(handle_select_args(h, a.logits, T, topk_ids, topk_w), st);
     if (e != cudaSuccess) return cuda_fail(h, e, "moe_route");
     if (h->prof[1]) cudaEventRecord(h->prof[1], st);
     return MOE_OK;
@@ -467,7 +496,8 @@ moe_status moe_route_from_logits(moe_handle h, const float* logits, int32_t T, i
     a.ids = topk_ids;
     a.w = topk_w;
     a.T = T; a.H = h->cfg.hidden; a.E = h->cfg.num_experts; a.k = h->cfg.top_k;
-    cudaError_t e = launch_route(a, (cudaStream_t)stream);
+    cudaError_t e = h->rule_set ? launch_select(handle_select_args(h, logits, T, topk_ids, topk_w), (cudaStream_t)stream)
+                                : launch_route(a, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "moe_route_from_logits");
     return MOE_OK;
 }
@@ -640,7 +670,7 @@ moe_status moe_route_forward(moe_handle h, const void* x, int32_t T, int32_t* to
     cudaError_t pe = cudaSuccess;
     const bool fused = use_fused_decode(h, st, &pe);
     if (pe != cudaSuccess) return cuda_fail(h, pe, "moe_route_forward");
-    if (!fused || T > 8 || !decode_supported(T, c.top_k)) {
+    if (!fused || h->rule_set || T > 8 || !decode_supported(T, c.top_k)) {
         s = moe_route(h, x, T, topk_ids, topk_w, nullptr, stream);
         if (s != MOE_OK) return s;
         return moe_forward(h, x, T, topk_ids, topk_w, y, stream);
@@ -874,6 +904,250 @@ moe_status moe_set_expert_table(moe_handle h, const void* const* blocks, moe_str
     if (e == cudaSuccess && blocks) e = cudaStreamSynchronize((cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "moe_set_expert_table");
     h->table_set = blocks != nullptr;
+    return MOE_OK;
+}
+
+// ------------------------------------------------------- around the experts
+
+// Do rows p[T][wp] (lp apart) and q[T][wq] (lq apart), all in bytes, share a
+// byte?  Rows of one matrix side by side (equal distances) do not; row ranges
+// that interleave otherwise count as shared.
+static bool rows_overlap(const void* p, int64_t lp, int64_t wp, const void* q, int64_t lq, int64_t wq, int64_t T) {
+    const int64_t a = (int64_t)(uintptr_t)p, b = (int64_t)(uintptr_t)q;
+    if (a + (T - 1) * lp + wp <= b || b + (T - 1) * lq + wq <= a) return false;
+    if (lp != lq || T == 1) return true;
+    const int64_t d = ((b - a) % lp + lp) % lp;      // q's first column inside p's rows
+    return d < wp || d + wq > lp;
+}
+
+static bool bad_rows(const void* p, int64_t ld, int64_t width, int32_t T, int elem_bytes) {
+    return !aligned16(p) || (T > 1 && (ld < width || (ld * elem_bytes) % 16 != 0 || ld > (int64_t)1 << 40));
+}
+
+static moe_status check_rule(moe_layer* h, const char* fn, const moe_routing* r, int32_t E, int32_t k) {
+    if (E < 1 || E > 1024 || k < 1 || k > 32 || k > E)
+        return fail(h, MOE_ERR_UNSUPPORTED, "%s: need 1 <= E <= 1024 and 1 <= k <= min(E, 32)", fn);
+    if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: unknown score %d", fn, r->score);
+    if (r->group_score != MOE_GROUP_MAX && r->group_score != MOE_GROUP_TOP2)
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: unknown group score %d", fn, r->group_score);
+    if (r->num_groups > 32) return fail(h, MOE_ERR_UNSUPPORTED, "%s: at most 32 groups", fn);
+    if (r->num_groups < 1 || E % r->num_groups || r->top_groups < 1 || r->top_groups > r->num_groups)
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: num_groups must divide E and top_groups lie in [1, num_groups]", fn);
+    if (r->top_groups * (E / r->num_groups) < k)
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: top_groups hold fewer than k experts", fn);
+    if (r->renorm != 0 && r->renorm != 1) return fail(h, MOE_ERR_INVALID_ARG, "%s: renorm must be 0 or 1", fn);
+    if (!isfinite(r->scale)) return fail(h, MOE_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    return MOE_OK;
+}
+
+moe_status moe_select_experts(const float* logits, int64_t ld_logits, int32_t T, int32_t E, int32_t k,
+                              const moe_routing* rule, int32_t* topk_ids, float* topk_w, moe_stream_t stream) {
+    if (!rule) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: null rule");
+    const moe_status s = check_rule(nullptr, "moe_select_experts", rule, E, k);
+    if (s != MOE_OK) return s;
+    if (T < 0) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: negative T");
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_ids || !topk_w) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: null pointer");
+    if (T > 1 && (ld_logits < E || ld_logits > (int64_t)1 << 40))
+        return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: ld_logits below E");
+    const cudaError_t e = launch_select(select_args(logits, ld_logits, T, E, k, *rule, rule->bias, topk_ids, topk_w),
+                                        (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(nullptr, e, "moe_select_experts");
+    return MOE_OK;
+}
+
+moe_status moe_set_routing(moe_handle h, const moe_routing* rule, moe_stream_t stream) {
+    if (!h) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_set_routing: null handle");
+    if (!rule) {
+        h->rule_set = false;
+        return MOE_OK;
+    }
+    const moe_status s = check_rule(h, "moe_set_routing", rule, h->cfg.num_experts, h->cfg.top_k);
+    if (s != MOE_OK) return s;
+    DeviceGuard dg(h->cfg.device);
+    if (rule->bias) {
+        const cudaError_t e = cudaMemcpyAsync(h->rule_bias, rule->bias, sizeof(float) * (size_t)h->cfg.num_experts,
+                                              cudaMemcpyDefault, (cudaStream_t)stream);
+        if (e != cudaSuccess) return cuda_fail(h, e, "moe_set_routing");
+    }
+    h->rule = *rule;
+    h->rule_set = true;
+    return MOE_OK;
+}
+
+static moe_status check_adapters(moe_layer* h, const char* fn, const moe_adapters* ad) {
+    if (!ad || !ad->a || !ad->b || !ad->scales) return fail(h, MOE_ERR_INVALID_ARG, "%s: null adapters", fn);
+    if (ad->num_adapters < 1) return fail(h, MOE_ERR_INVALID_ARG, "%s: num_adapters must be positive", fn);
+    if (ad->R < 8 || ad->R > kAdapterMaxRank || ad->R % 8 || ad->K < 8 || ad->K % 8 || ad->N < 8 || ad->N % 8)
+        return fail(h, MOE_ERR_UNSUPPORTED, "%s: R, K and N must be positive multiples of 8, R at most %d", fn,
+                    kAdapterMaxRank);
+    if (!aligned16(ad->a) || !aligned16(ad->b))
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: a and b must be 16-byte aligned", fn);
+    return MOE_OK;
+}
+
+static AdapterArgs adapter_args(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,
+                                int32_t wide, int32_t T, const int32_t* ids, const moe_adapters* ad) {
+    AdapterArgs a{};
+    a.x = x; a.y = y; a.out = out; a.ids = ids;
+    a.a = ad->a; a.b = ad->b; a.scales = ad->scales; a.ranks = ad->ranks;
+    a.ld_x = ld_x; a.ld_y = ld_y; a.ld_out = ld_out;
+    a.T = T; a.K = ad->K; a.N = ad->N; a.R = ad->R; a.n = ad->num_adapters;
+    a.wide = wide != 0;
+    return a;
+}
+
+moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,
+                            int32_t y_fp32, int32_t T, const int32_t* adapter_ids, const moe_adapters* ad,
+                            moe_stream_t stream) {
+    const char* fn = "moe_add_adapters";
+    const moe_status s = check_adapters(nullptr, fn, ad);
+    if (s != MOE_OK) return s;
+    if (T < 0) return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: negative T", fn);
+    if (T == 0) return MOE_OK;
+    if (!x || !y || !out || !adapter_ids) return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const int es = y_fp32 ? 4 : 2;
+    if (bad_rows(x, ld_x, ad->K, T, 2) || bad_rows(y, ld_y, ad->N, T, es) || bad_rows(out, ld_out, ad->N, T, es))
+        return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and at least their width apart", fn);
+    const bool in_place = out == y && (ld_out == ld_y || T == 1);
+    if (rows_overlap(x, ld_x * 2, (int64_t)ad->K * 2, out, ld_out * es, (int64_t)ad->N * es, T) ||
+        (!in_place && rows_overlap(y, ld_y * es, (int64_t)ad->N * es, out, ld_out * es, (int64_t)ad->N * es, T)))
+        return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
+    const cudaError_t e = launch_add_adapters(adapter_args(x, ld_x, y, ld_y, out, ld_out, y_fp32, T, adapter_ids, ad),
+                                              (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(nullptr, e, fn);
+    return MOE_OK;
+}
+
+// the arguments of moe_block_norm (h: whose error text a failure sets)
+static moe_status check_norm(moe_layer* h, const char* fn, const moe_norm* n) {
+    if (n->H < 8 || n->H % 8 || n->H > 16384)
+        return fail(h, MOE_ERR_UNSUPPORTED, "%s: H must be a multiple of 8 in [8, 16384]", fn);
+    if (n->T < 0) return fail(h, MOE_ERR_INVALID_ARG, "%s: negative T", fn);
+    if (n->T == 0) return MOE_OK;
+    if (!n->r || (!n->r_out && !n->x_out) || (!n->x_out) != (!n->w_pre))
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: need r, an output, and w_pre exactly with x_out", fn);
+    if (n->gate_kind < MOE_GATE_NONE || n->gate_kind > MOE_GATE_ELEMENT)
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: unknown gate kind %d", fn, n->gate_kind);
+    if ((n->gate_kind != MOE_GATE_NONE) != (n->gate != nullptr))
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: gate and gate_kind must go together", fn);
+    if (!n->y && (n->w_post || n->gate)) return fail(h, MOE_ERR_INVALID_ARG, "%s: w_post and gate need y", fn);
+    if (!(n->eps > 0.0f) || !isfinite(n->eps) || !isfinite(n->branch_scale) || !isfinite(n->residual_scale))
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: eps must be positive, eps and the scales finite", fn);
+    const int es = n->r_fp32 ? 4 : 2;
+    if (bad_rows(n->r, n->ld_r, n->H, n->T, es) || (n->y && bad_rows(n->y, n->ld_y, n->H, n->T, 2)) ||
+        (n->r_out && bad_rows(n->r_out, n->ld_r_out, n->H, n->T, es)) ||
+        (n->x_out && bad_rows(n->x_out, n->ld_x, n->H, n->T, 2)) ||
+        (n->gate_kind == MOE_GATE_ELEMENT && bad_rows(n->gate, n->ld_gate, n->H, n->T, 2)) ||
+        !aligned16(n->w_post) || !aligned16(n->w_pre) || (n->gate_kind == MOE_GATE_CHANNEL && !aligned16(n->gate)))
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and at least H apart", fn);
+    const int64_t T = n->T, w2 = (int64_t)n->H * 2, wr = (int64_t)n->H * es;
+    struct Rows { const void* p; int64_t ld, w; };
+    const Rows r{n->r, n->ld_r * es, wr}, y{n->y, n->ld_y * 2, w2}, ro{n->r_out, n->ld_r_out * es, wr},
+        xo{n->x_out, n->ld_x * 2, w2}, g{n->gate_kind == MOE_GATE_ELEMENT ? n->gate : nullptr, n->ld_gate * 2, w2};
+    auto clash = [&](const Rows& a, const Rows& b) {
+        return a.p && b.p && rows_overlap(a.p, a.ld, a.w, b.p, b.ld, b.w, T);
+    };
+    auto same = [&](const Rows& a, const Rows& b) { return a.p == b.p && (a.ld == b.ld || T == 1); };
+    if ((!same(ro, r) && clash(ro, r)) || (!same(xo, y) && clash(xo, y)) || clash(ro, y) || clash(xo, r) || clash(ro, xo) ||
+        clash(ro, g) || clash(xo, g))
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: an output overlaps another tensor", fn);
+    return MOE_OK;
+}
+
+static cudaError_t run_norm(const moe_norm* n, cudaStream_t st) {
+    NormArgs a{};
+    a.r = n->r; a.y = n->y; a.w_post = n->w_post; a.gate = n->gate; a.w_pre = n->w_pre;
+    a.r_out = n->r_out; a.x_out = n->x_out;
+    a.ld_r = n->ld_r; a.ld_y = n->ld_y; a.ld_gate = n->ld_gate; a.ld_r_out = n->ld_r_out; a.ld_x = n->ld_x;
+    a.T = n->T; a.H = n->H; a.gate_kind = n->gate_kind;
+    a.r_fp32 = n->r_fp32 != 0; a.gate_sigmoid = n->gate_sigmoid != 0;
+    a.eps = n->eps; a.branch_scale = n->branch_scale; a.residual_scale = n->residual_scale;
+    a.offset = n->unit_offset ? 1.0f : 0.0f;
+    return launch_block_norm(a, st);
+}
+
+moe_status moe_block_norm(const moe_norm* norm, moe_stream_t stream) {
+    if (!norm) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_block_norm: null argument");
+    const moe_status s = check_norm(nullptr, "moe_block_norm", norm);
+    if (s != MOE_OK || norm->T == 0) return s;
+    const cudaError_t e = run_norm(norm, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(nullptr, e, "moe_block_norm");
+    return MOE_OK;
+}
+
+moe_status moe_block_forward(moe_handle h, const moe_block* b, moe_stream_t stream) {
+    const char* fn = "moe_block_forward";
+    if (!h) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_block_forward: null handle");
+    if (!b) return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: null block");
+    moe_status s = check_tokens(h, fn, b->T);
+    if (s != MOE_OK) return s;
+    const moe_config& c = h->cfg;
+    const int32_t H = c.hidden, T = b->T;
+    if (!b->r || !b->x || !b->y || !b->topk_ids || !b->topk_w)
+        return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: null pointer");
+    if (!aligned16(b->r) || !aligned16(b->x) || !aligned16(b->y))
+        return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: r, x and y must be 16-byte aligned");
+    const int64_t w2 = (int64_t)H * 2, wr = (int64_t)H * (b->r_fp32 ? 4 : 2);
+    if (rows_overlap(b->x, w2, w2, b->y, w2, w2, T) || rows_overlap(b->r, wr, wr, b->x, w2, w2, T) ||
+        rows_overlap(b->r, wr, wr, b->y, w2, w2, T))
+        return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: r, x and y must not overlap");
+    const moe_adapters* ads[2] = {b->router_adapters, b->layer_adapters};
+    for (int i = 0; i < 2; ++i) {
+        if (!ads[i]) continue;
+        if ((s = check_adapters(h, fn, ads[i])) != MOE_OK) return s;
+        if (!b->adapter_ids) return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: adapters without adapter_ids");
+        if (ads[i]->K != H || ads[i]->N != (i == 0 ? c.num_experts : H))
+            return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: adapter shapes must be H -> %s", i == 0 ? "E" : "H");
+    }
+    if (b->router_adapters && b->logits && !aligned16(b->logits))
+        return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: logits must be 16-byte aligned");
+    moe_norm n{};
+    n.r = b->r; n.T = T; n.H = H; n.r_fp32 = b->r_fp32;
+    n.ld_r = n.ld_y = n.ld_gate = n.ld_r_out = n.ld_x = H;
+    n.unit_offset = b->unit_offset; n.eps = b->eps;
+    n.branch_scale = b->branch_scale;
+    n.residual_scale = 1.0f;
+    moe_norm in = n;
+    in.w_pre = b->w_in; in.x_out = b->x;
+    n.y = b->y; n.w_post = b->w_post; n.gate = b->gate; n.gate_kind = b->gate_kind; n.gate_sigmoid = b->gate_sigmoid;
+    n.w_pre = b->w_next; n.r_out = b->r; n.x_out = b->x_next;
+    n.residual_scale = b->residual_scale;
+    if (b->w_in && (s = check_norm(h, fn, &in)) != MOE_OK) return s;
+    if ((s = check_norm(h, fn, &n)) != MOE_OK) return s;
+    // the states that moe_route and moe_forward need
+    if (!h->router_loaded) return fail(h, MOE_ERR_STATE, "moe_block_forward: router not loaded");
+    if (h->experts_loaded != c.num_experts)
+        return fail(h, MOE_ERR_STATE, "moe_block_forward: %d of %d experts loaded", h->experts_loaded, c.num_experts);
+    if (c.has_shared && !h->shared_loaded) return fail(h, MOE_ERR_STATE, "moe_block_forward: shared expert not loaded");
+    if (c.quant == MOE_Q_NVFP4 && !h->act_scales_set)
+        return fail(h, MOE_ERR_STATE, "moe_block_forward: NVFP4 activation global scales not set");
+    DeviceGuard dg(c.device);
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = cudaSuccess;
+    if (b->w_in && (e = run_norm(&in, st)) != cudaSuccess) return cuda_fail(h, e, fn);
+    if (b->router_adapters) {
+        const int32_t E = c.num_experts;
+        float* logits = b->logits ? b->logits : h->logits;
+        s = moe_route(h, b->x, T, nullptr, nullptr, logits, stream);
+        if (s != MOE_OK) return s;
+        e = launch_add_adapters(adapter_args(b->x, H, logits, E, logits, E, 1, T, b->adapter_ids, b->router_adapters), st);
+        if (e != cudaSuccess) return cuda_fail(h, e, fn);
+        s = moe_route_from_logits(h, logits, T, b->topk_ids, b->topk_w, stream);
+        if (s == MOE_OK) s = moe_forward(h, b->x, T, b->topk_ids, b->topk_w, b->y, stream);
+    } else if (b->logits) {
+        s = moe_route(h, b->x, T, b->topk_ids, b->topk_w, b->logits, stream);
+        if (s == MOE_OK) s = moe_forward(h, b->x, T, b->topk_ids, b->topk_w, b->y, stream);
+    } else {
+        s = moe_route_forward(h, b->x, T, b->topk_ids, b->topk_w, b->y, stream);
+    }
+    if (s != MOE_OK) return s;
+    if (b->layer_adapters) {
+        e = launch_add_adapters(adapter_args(b->x, H, b->y, H, b->y, H, 0, T, b->adapter_ids, b->layer_adapters), st);
+        if (e != cudaSuccess) return cuda_fail(h, e, fn);
+    }
+    if ((e = run_norm(&n, st)) != cudaSuccess) return cuda_fail(h, e, fn);
     return MOE_OK;
 }
 

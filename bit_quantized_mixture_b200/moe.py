@@ -21,6 +21,11 @@ QUANT = {"int4": 0, "int2": 1, "nvfp4": 2, "bf16": 3, "int4g32": 4, "fp8": 5, "f
 SHARED = -1
 
 
+SCORE = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
+GATE = {"none": 0, "channel": 1, "token": 2, "element": 3}
+
+
 class MoeError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"[{status}] {msg}")
@@ -39,6 +44,32 @@ class QMatrix(ctypes.Structure):
 
 class ExpertWeights(ctypes.Structure):
     _fields_ = [("gate", QMatrix), ("up", QMatrix), ("down", QMatrix)]
+
+
+class RoutingRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
+class AdapterSet(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ranks", ctypes.c_void_p),
+                ("num_adapters", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("r", "y", "w_post", "gate", "w_pre", "r_out", "x_out")] + \
+               [(n, ctypes.c_int64) for n in ("ld_r", "ld_y", "ld_gate", "ld_r_out", "ld_x")] + \
+               [(n, ctypes.c_int32) for n in ("T", "H", "r_fp32", "gate_kind", "gate_sigmoid", "unit_offset")] + \
+               [(n, ctypes.c_float) for n in ("eps", "branch_scale", "residual_scale")]
+
+
+class Block(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("r", "x", "y", "x_next", "w_in", "w_post", "w_next", "gate", "logits",
+                                               "topk_ids", "topk_w", "adapter_ids")] + \
+               [("router_adapters", ctypes.POINTER(AdapterSet)), ("layer_adapters", ctypes.POINTER(AdapterSet))] + \
+               [(n, ctypes.c_int32) for n in ("T", "r_fp32", "gate_kind", "gate_sigmoid", "unit_offset")] + \
+               [(n, ctypes.c_float) for n in ("eps", "branch_scale", "residual_scale")]
 
 
 _lib = None
@@ -77,6 +108,11 @@ def lib():
             "moe_debug_get_permutation": [vp, vp, vp, vp, vp, vp],
             "moe_debug_get_act_nvfp4": [vp, vp, vp, vp],
             "moe_debug_set_wait_test": [vp, i32, i64],
+            "moe_select_experts": [vp, i64, i32, i32, i32, ctypes.POINTER(RoutingRule), vp, vp, vp],
+            "moe_set_routing": [vp, ctypes.POINTER(RoutingRule), vp],
+            "moe_add_adapters": [vp, i64, vp, i64, vp, i64, i32, i32, vp, ctypes.POINTER(AdapterSet), vp],
+            "moe_block_norm": [ctypes.POINTER(Norm), vp],
+            "moe_block_forward": [vp, ctypes.POINTER(Block), vp],
             "moe_mma_peak_loop": [i32, i32, i64, vp, ctypes.POINTER(ctypes.c_double), vp],
         }
         for name, args in sig.items():
@@ -113,6 +149,170 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _refuse(msg):
+    raise MoeError(MOE_ERR_INVALID_ARG, msg)
+
+
+def _cuda(name, t, dtype, shape, dev=None):
+    """A contiguous CUDA tensor of this dtype and shape, on device dev."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or tuple(t.shape) != shape or \
+            not t.is_contiguous() or (dev is not None and t.device != dev):
+        _refuse(f"{name}: need a contiguous {dtype} CUDA tensor {list(shape)}" + (f" on {dev}" if dev is not None else ""))
+    return t.data_ptr()
+
+
+def _rows(name, t, dtypes, shape, dev):
+    """(address, elements between rows) of a 2-D CUDA tensor whose rows are
+    contiguous; shape entries may be None."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or \
+            (dev is not None and t.device != dev):
+        _refuse(f"{name}: need a 2-D CUDA tensor of {', '.join(str(d) for d in dtypes)}" +
+                (f" on {dev}" if dev is not None else ""))
+    T, W = t.shape
+    if (shape[0] is not None and T != shape[0]) or (shape[1] is not None and W != shape[1]):
+        _refuse(f"{name}: shape {list(t.shape)}, need {list(shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and W > 1:
+        _refuse(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), s0 if T > 1 else W
+
+
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+def _on(dev, stream):
+    """(guard, raw stream) of a call on dev's tensors: the guard makes dev
+    current where it is not (null when it is)."""
+    guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    return guard, stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _call(fn, dev, stream, *args):
+    guard, raw = _on(dev, stream)
+    if guard is None:
+        status = fn(*args, raw)
+    else:
+        with guard:
+            status = fn(*args, raw)
+    if status != MOE_OK:
+        _check(status)
+
+
+def _new(shape, dtype, dev, stream):
+    """An output tensor; with a stream of its own it belongs to that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+class Routing:
+    """A routing rule (moe_routing): scores, selection bias (fp32 [E] CUDA
+    tensor, kept alive here), groups, renormalisation and scale."""
+
+    def __init__(self, score="softmax", bias=None, num_groups=1, top_groups=1, group_score="max", renorm=True, scale=1.0):
+        if score not in SCORE or group_score not in GROUP_SCORE:
+            _refuse(f"Routing: score must be one of {list(SCORE)}, group_score one of {list(GROUP_SCORE)}")
+        if bias is not None and bias.dim() != 1:
+            _refuse("Routing: bias must be [E]")
+        self.bias = bias
+        self.c = RoutingRule(SCORE[score], num_groups, top_groups, GROUP_SCORE[group_score], int(bool(renorm)), scale,
+                             _cuda("bias", bias, torch.float32, tuple(bias.shape)) if bias is not None else None)
+
+
+def select_experts(logits, k, rule, ids=None, w=None, stream=None):
+    """fp32 logits [T, E] -> (ids int32 [T, k], weights fp32 [T, k]) under a
+    Routing rule (moe_select_experts)."""
+    ptr, ld = _rows("logits", logits, _F32, (None, None), None)
+    T, E = logits.shape
+    dev = logits.device
+    if rule.bias is not None and (rule.bias.shape[0] != E or rule.bias.device != dev):
+        _refuse(f"bias: need {E} entries on {dev}")
+    if ids is None:
+        ids = _new((T, k), torch.int32, dev, stream)
+    if w is None:
+        w = _new((T, k), torch.float32, dev, stream)
+    _call(lib().moe_select_experts, dev, stream, ptr, ld, T, E, k, rule.c,
+          _cuda("ids", ids, torch.int32, (T, k), dev), _cuda("w", w, torch.float32, (T, k), dev))
+    return ids, w
+
+
+def _adapter_set(a, b, scales, ranks, dev):
+    if not isinstance(a, torch.Tensor) or a.dim() != 3 or not isinstance(b, torch.Tensor) or b.dim() != 3:
+        _refuse("a and b: need [n, R, K] and [n, N, R]")
+    n, R, K = a.shape
+    N = b.shape[1]
+    return AdapterSet(_cuda("a", a, torch.bfloat16, (n, R, K), dev), _cuda("b", b, torch.bfloat16, (n, N, R), dev),
+                      _cuda("scales", scales, torch.float32, (n,), dev),
+                      None if ranks is None else _cuda("ranks", ranks, torch.int32, (n,), dev), n, R, K, N)
+
+
+def add_adapters(x, y, adapter_ids, a, b, scales, ranks=None, out=None, stream=None):
+    """out_t = y_t + scales[i] b_i (a_i x_t), i = adapter_ids[t]
+    (moe_add_adapters): x bf16 [T, K], y bf16 or fp32 [T, N], a bf16
+    [n, R, K], b bf16 [n, N, R], scales fp32 [n], ranks int32 [n] or None.
+    out may be y; by default it is a new tensor."""
+    xp, ldx = _rows("x", x, _BF16, (None, None), None)
+    T, K = x.shape
+    dev = x.device
+    c = _adapter_set(a, b, scales, ranks, dev)
+    if c.K != K:
+        _refuse(f"a: {c.K} columns, x has {K}")
+    yp, ldy = _rows("y", y, _BF16_F32, (T, c.N), dev)
+    if out is None:
+        out = _new((T, c.N), y.dtype, dev, stream)
+    op, ldo = _rows("out", out, (y.dtype,), (T, c.N), dev)
+    _call(lib().moe_add_adapters, dev, stream, xp, ldx, yp, ldy, op, ldo, int(y.dtype is torch.float32), T,
+          _cuda("adapter_ids", adapter_ids, torch.int32, (T,), dev), c)
+    return out
+
+
+def _gate(gate, T, H, dev):
+    """(kind, address, elements between rows) of a gate tensor by its shape."""
+    if gate is None:
+        return GATE["none"], None, 0
+    if gate.dim() == 2:
+        return (GATE["element"],) + _rows("gate", gate, _BF16, (T, H), dev)
+    if gate.dtype is torch.float32:
+        return GATE["token"], _cuda("gate", gate, torch.float32, (T,), dev), 0
+    return GATE["channel"], _cuda("gate", gate, torch.bfloat16, (H,), dev), 0
+
+
+def block_norm(r, y=None, post_weight=None, gate=None, gate_sigmoid=False, pre_weight=None, eps=1e-6, branch_scale=1.0,
+               residual_scale=1.0, unit_offset=False, r_out=None, x_out=None, stream=None):
+    """The norms, gate and residual add between two blocks (moe_block_norm):
+    r bf16 or fp32 [T, H], y bf16 [T, H], weights bf16 [H]; gate bf16 [H]
+    (channel), fp32 [T] (token) or bf16 [T, H] (element).  Returns (r', x);
+    x is None without pre_weight.  r_out may be r, x_out may be y."""
+    rp, ldr = _rows("r", r, _BF16_F32, (None, None), None)
+    T, H = r.shape
+    dev = r.device
+    n = Norm(r=rp, ld_r=ldr, T=T, H=H, r_fp32=r.dtype is torch.float32, gate_sigmoid=bool(gate_sigmoid),
+             unit_offset=bool(unit_offset), eps=eps, branch_scale=branch_scale, residual_scale=residual_scale)
+    if y is not None:
+        n.y, n.ld_y = _rows("y", y, _BF16, (T, H), dev)
+    if post_weight is not None:
+        n.w_post = _cuda("post_weight", post_weight, torch.bfloat16, (H,), dev)
+    n.gate_kind, n.gate, n.ld_gate = _gate(gate, T, H, dev)
+    if r_out is None:
+        r_out = _new((T, H), r.dtype, dev, stream)
+    n.r_out, n.ld_r_out = _rows("r_out", r_out, (r.dtype,), (T, H), dev)
+    if pre_weight is not None:
+        n.w_pre = _cuda("pre_weight", pre_weight, torch.bfloat16, (H,), dev)
+        if x_out is None:
+            x_out = _new((T, H), torch.bfloat16, dev, stream)
+        n.x_out, n.ld_x = _rows("x_out", x_out, _BF16, (T, H), dev)
+    elif x_out is not None:
+        _refuse("x_out: needs pre_weight")
+    _call(lib().moe_block_norm, dev, stream, n)
+    return r_out, x_out
 
 
 def nvfp4_global_scale(amax: float) -> float:
@@ -178,6 +378,48 @@ class MoeLayer:
         """The whole layer (route + forward) in one call."""
         _check(lib().moe_route_forward(self.h, _ptr(x), x.shape[0], _ptr(ids), _ptr(w), _ptr(y), _stream(stream)),
                self.h)
+
+    def set_routing(self, rule, stream=None):
+        """Follow a Routing rule in route, route_from_logits, route_forward and
+        block_forward (None: softmax and top-k again)."""
+        if rule is not None and rule.bias is not None and rule.bias.shape[0] != self.cfg.num_experts:
+            _refuse(f"bias: need {self.cfg.num_experts} entries")
+        _check(lib().moe_set_routing(self.h, rule.c if rule is not None else None, _stream(stream)), self.h)
+        self._rule = rule          # its bias outlives the asynchronous copy
+
+    def block_forward(self, r, x, y, ids, w, w_in=None, w_post=None, w_next=None, x_next=None, gate=None,
+                      gate_sigmoid=False, logits=None, adapter_ids=None, router_adapters=None, layer_adapters=None,
+                      eps=1e-6, branch_scale=1.0, residual_scale=1.0, unit_offset=False, stream=None):
+        """One MoE block (moe_block_forward): x = norm(r, w_in), the layer x -> y
+        with its adapters, r and x_next = block_norm(r, y).  Adapters are
+        (a, b, scales, ranks or None) tuples; r is updated in place."""
+        dev = torch.device("cuda", self.cfg.device)
+        H, E, k = self.cfg.hidden, self.cfg.num_experts, self.cfg.top_k
+        T = r.shape[0]
+        if r.dtype not in _BF16_F32:
+            _refuse("r: need bf16 or fp32")
+        bf = torch.bfloat16
+        b = Block(r=_cuda("r", r, r.dtype, (T, H), dev), x=_cuda("x", x, bf, (T, H), dev), y=_cuda("y", y, bf, (T, H), dev),
+                  topk_ids=_cuda("ids", ids, torch.int32, (T, k), dev), topk_w=_cuda("w", w, torch.float32, (T, k), dev),
+                  T=T, r_fp32=r.dtype is torch.float32, gate_sigmoid=bool(gate_sigmoid), unit_offset=bool(unit_offset),
+                  eps=eps, branch_scale=branch_scale, residual_scale=residual_scale)
+        for name, t in (("w_in", w_in), ("w_post", w_post), ("w_next", w_next)):
+            if t is not None:
+                setattr(b, name, _cuda(name, t, bf, (H,), dev))
+        if x_next is not None:
+            b.x_next = _cuda("x_next", x_next, bf, (T, H), dev)
+        if logits is not None:
+            b.logits = _cuda("logits", logits, torch.float32, (T, E), dev)
+        b.gate_kind, b.gate, ld_gate = _gate(gate, T, H, dev)
+        if b.gate_kind == GATE["element"] and ld_gate != H:
+            _refuse("gate: need contiguous rows")
+        if adapter_ids is not None:
+            b.adapter_ids = _cuda("adapter_ids", adapter_ids, torch.int32, (T,), dev)
+        if router_adapters is not None:
+            b.router_adapters = ctypes.pointer(_adapter_set(*router_adapters, dev))
+        if layer_adapters is not None:
+            b.layer_adapters = ctypes.pointer(_adapter_set(*layer_adapters, dev))
+        _check(lib().moe_block_forward(self.h, b, _stream(stream)), self.h)
 
     def set_profile_events(self, events):
         """events: 5 to 10 torch.cuda.Event(enable_timing=True) (recorded once

@@ -295,6 +295,149 @@ moe_status moe_export_expert(moe_handle h, int32_t expert, void* dst, moe_stream
  * Errors: INVALID_ARG (null or misaligned entry: nothing changes), CUDA. */
 moe_status moe_set_expert_table(moe_handle h, const void* const* blocks, moe_stream_t stream);
 
+/* ------------------------------------------------- around the experts
+ *
+ * Expert selection by other rules than softmax + top-k, low-rank adapters of
+ * many requests, and the norms, gate and residual add between two blocks.
+ * The pages' checkpoints need none of them; other sparse models with the same
+ * experts do.  All are forward operators (the layer serves frozen weights).
+ * The calls without a handle run on the current device, which the pointers
+ * belong to; T = 0 is a no-op.  Rows are `ld` elements apart (at least the
+ * row's width; any value when T <= 1); bf16 and fp32 rows other than logits
+ * start on 16-byte boundaries (ld a multiple of 8 for bf16, of 4 for fp32). */
+
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0        /* a group's score: its largest key */
+#define MOE_GROUP_TOP2 1       /* ... the sum of its two largest keys (of one, where it has one) */
+
+/* A routing rule.  Per token, with logits l_e:
+ *   eligible: l_e and bias_e are above the lowest finite fp32 value: NaN,
+ *             -inf and that value (as masks hold them) switch an expert off;
+ *             +inf counts as the largest finite value
+ *   s_e   = softmax over the eligible experts, or 1 / (1 + exp(-l_e))
+ *   key_e = s_e + bias_e; without a bias the keys' order is the logits' order
+ *   groups of E / num_groups consecutive experts; the top_groups best by
+ *           group_score stay (the lower group on ties, groups without an
+ *           eligible expert last)
+ *   ids   = the k best keys of the groups that stay, key descending, expert
+ *           ascending on equal keys; slots that find no eligible expert take
+ *           the lowest-numbered experts not chosen, with weight 0, so that the
+ *           ids stay distinct and valid for moe_forward (a fully masked token
+ *           gets experts 0 .. k-1 and weights 0)
+ *   w_j   = scale * s_j, divided by the sum of the chosen s when renorm is set
+ * The order is that of the exact keys, not of their fp32 roundings. */
+typedef struct {
+    int32_t score;             /* MOE_SCORE_* */
+    int32_t num_groups;        /* 1 (no groups) .. 32, dividing E */
+    int32_t top_groups;        /* 1 .. num_groups, with top_groups * E / num_groups >= k */
+    int32_t group_score;       /* MOE_GROUP_* */
+    int32_t renorm;            /* 1: weights divided by their sum */
+    float scale;               /* finite; multiplies the weights */
+    const float* bias;         /* fp32 [E] or NULL; selection only */
+} moe_routing;
+
+/* ids int32 [T, k] and weights fp32 [T, k] of fp32 logits [T, E] under
+ * `rule` (bias on the device).  1 <= E <= 1024, 1 <= k <= min(E, 32).
+ * Errors: INVALID_ARG, UNSUPPORTED (E, k or num_groups), CUDA. */
+moe_status moe_select_experts(const float* logits, int64_t ld_logits, int32_t T, int32_t E, int32_t k,
+                              const moe_routing* rule, int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+
+/* moe_route, moe_route_from_logits and moe_route_forward of this handle
+ * follow `rule` from now on (NULL: softmax + top-k again).  The bias (host or
+ * device) is copied on `stream` into the handle; calls on other streams wait
+ * for that copy themselves.  With a rule, moe_route_forward runs the router,
+ * the selection and moe_forward instead of the one fused kernel.
+ * Errors: as moe_select_experts, for the handle's E and k. */
+moe_status moe_set_routing(moe_handle h, const moe_routing* rule, moe_stream_t stream);
+
+/* Low-rank adapters of many requests beside one projection K -> N. */
+typedef struct {
+    const void* a;             /* bf16 [n][R][K] */
+    const void* b;             /* bf16 [n][N][R] */
+    const float* scales;       /* fp32 [n] */
+    const int32_t* ranks;      /* int32 [n]: rows of a[i] / columns of b[i] in use (clamped to 0 .. R; the
+                                  others are not used, whatever they hold), or NULL: all R */
+    int32_t num_adapters;      /* n >= 1 */
+    int32_t R;                 /* multiple of 8, 8 .. 128 */
+    int32_t K, N;              /* multiples of 8 */
+} moe_adapters;
+
+/* out_t = y_t + scales[i] * b_i (a_i x_t) with i = adapter_ids[t]; a token
+ * whose id lies outside [0, n), or whose adapter has rank 0, keeps y_t bit
+ * for bit.  x bf16 [T, K]; y and out [T, N], both bf16 or (y_fp32) both
+ * fp32; out may be y itself (same ld) and otherwise overlaps no input.
+ * Products and sums are fp32, out is rounded once.  With more than a few
+ * tokens the second product's operand, scale * a x, is held in bf16 for bf16
+ * outputs and in two bf16 halves (16 significant bits) for fp32 outputs.
+ * Deterministic; needs no workspace.
+ * Errors: INVALID_ARG, UNSUPPORTED (R, K or N), CUDA. */
+moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,
+                            int32_t y_fp32, int32_t T, const int32_t* adapter_ids, const moe_adapters* adapters,
+                            moe_stream_t stream);
+
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1     /* bf16 [H] */
+#define MOE_GATE_TOKEN 2       /* fp32 [T] */
+#define MOE_GATE_ELEMENT 3     /* bf16 [T, H] */
+
+/* The norms, gate and residual add between two blocks, one pass over T rows:
+ *   u  = y * rsqrt(mean(y^2) + eps) * (w_post + o)      (u = y without w_post)
+ *   g  = 1, gate, or 1 / (1 + exp(-gate)) with gate_sigmoid
+ *   r' = residual_scale * r + branch_scale * g * u       (no y: the first term)
+ *   x  = r' * rsqrt(mean(r'^2) + eps) * (w_pre + o), from r' before its
+ *        rounding; o = 1 with unit_offset, else 0
+ * in fp32 (a row's squares must not overflow it); r' and x are rounded once. */
+typedef struct {
+    const void* r;             /* bf16 or (r_fp32) fp32 [T, H] */
+    const void* y;             /* bf16 [T, H] or NULL */
+    const void* w_post;        /* bf16 [H] or NULL; needs y */
+    const void* gate;          /* by gate_kind; needs y */
+    const void* w_pre;         /* bf16 [H]; given exactly when x_out is */
+    void* r_out;               /* as r, or NULL; may be r itself */
+    void* x_out;               /* bf16 [T, H] or NULL; may be y itself */
+    int64_t ld_r, ld_y, ld_gate, ld_r_out, ld_x;   /* in elements */
+    int32_t T, H;              /* H: multiple of 8, 8 .. 16384 */
+    int32_t r_fp32, gate_kind, gate_sigmoid, unit_offset;
+    float eps;                 /* > 0 */
+    float branch_scale, residual_scale;
+} moe_norm;
+
+/* Errors: INVALID_ARG (null or misaligned pointers, strides, no output, an
+ * output that overlaps another tensor of the call otherwise than allowed),
+ * UNSUPPORTED (H), CUDA. */
+moe_status moe_block_norm(const moe_norm* norm, moe_stream_t stream);
+
+/* One MoE block of a model around the handle's layer, the calls above in
+ * their order of use:
+ *   x = norm of r by w_in                  (w_in given; else x is the input)
+ *   logits = x Wr^T (+ router_adapters), selection, y = moe_forward(x)
+ *   y += layer_adapters                    (K = N = H)
+ *   r, x_next = moe_block_norm(r, y)
+ * r is updated in place.  Rows are contiguous (ld = H). */
+typedef struct {
+    void* r;                   /* bf16 or (r_fp32) fp32 [T, H], in and out */
+    void* x;                   /* bf16 [T, H]: out with w_in, else in */
+    void* y;                   /* bf16 [T, H] out: the layer's output */
+    void* x_next;              /* bf16 [T, H] out or NULL: the next block's input */
+    const void* w_in;          /* bf16 [H] or NULL */
+    const void* w_post;        /* bf16 [H] or NULL */
+    const void* w_next;        /* bf16 [H]; given exactly when x_next is */
+    const void* gate;          /* as in moe_norm, ld_gate = H */
+    float* logits;             /* fp32 [T, E] out, or NULL: the handle's workspace */
+    int32_t* topk_ids;         /* int32 [T, k] out */
+    float* topk_w;             /* fp32 [T, k] out */
+    const int32_t* adapter_ids;            /* int32 [T]; needed with adapters */
+    const moe_adapters* router_adapters;   /* K = H, N = E, or NULL */
+    const moe_adapters* layer_adapters;    /* K = N = H, or NULL */
+    int32_t T, r_fp32, gate_kind, gate_sigmoid, unit_offset;
+    float eps, branch_scale, residual_scale;
+} moe_block;
+
+/* Errors: as the calls it is made of; nothing is enqueued on an argument or
+ * state error. */
+moe_status moe_block_forward(moe_handle h, const moe_block* block, moe_stream_t stream);
+
 /* ---------------------------------------------------------------- debug */
 
 /* Write loaded matrix `which` (0 gate, 1 up, 2 down) of `expert` back in

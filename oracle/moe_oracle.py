@@ -515,3 +515,88 @@ def intermediate_amax(x_bits, ids, quant, expert_fn, act_scale_x=None):
         Wg, Wu, _ = expert_fn(int(e))
         amax = max(amax, float(np.abs(swiglu_intermediate(X[tok], Wg, Wu)).max()))
     return amax
+
+
+# ------------------------------------------------------- around the experts
+# fp64 restatements of the operators around the layer, one token at a time.
+
+F32_MAX = float(np.finfo(np.float32).max)
+
+
+def select_experts(logits, k, score="softmax", bias=None, num_groups=1, top_groups=1, group_score="max", renorm=True,
+                   scale=1.0):
+    """Expert ids [T, k] and fp64 weights of fp32 logits [T, E] under a routing
+    rule.  NaN, -inf and the lowest finite fp32 value switch an expert off (as
+    a logit or as a bias); +inf counts as the largest finite value."""
+    logits = np.asarray(logits, dtype=np.float64)
+    T, E = logits.shape
+    ids = np.zeros((T, k), dtype=np.int32)
+    w = np.zeros((T, k))
+    per = E // num_groups
+    for t in range(T):
+        on = [e for e in range(E) if logits[t, e] > -F32_MAX and (bias is None or float(bias[e]) > -F32_MAX)]
+        x = {e: min(logits[t, e], F32_MAX) for e in on}
+        if score == "sigmoid":
+            s = {e: (1.0 / (1.0 + np.exp(-x[e])) if x[e] > -700 else 0.0) for e in on}
+        elif on:
+            top = max(x.values())
+            ex = {e: np.exp(x[e] - top) for e in on}
+            total = sum(ex.values())
+            s = {e: ex[e] / total for e in on}
+        key = {e: (x[e] if bias is None else s[e] + min(float(bias[e]), F32_MAX)) for e in on}
+        if num_groups > 1:
+            value = {}
+            for g in range(num_groups):
+                mine = [e for e in on if e // per == g]
+                if group_score == "top2" and per > 1:
+                    v = sorted(((s[e] if bias is None else key[e]) for e in mine), reverse=True)[:2]
+                    value[g] = sum(v) if v else -np.inf
+                else:
+                    value[g] = max((key[e] for e in mine), default=-np.inf)
+            kept = sorted(range(num_groups), key=lambda g: (-value[g], g))[:top_groups]
+            on = [e for e in on if e // per in kept]
+        chosen = sorted(on, key=lambda e: (-key[e], e))[:k]
+        rest = [e for e in range(E) if e not in chosen][: k - len(chosen)]
+        ids[t] = chosen + rest
+        if not chosen:
+            continue
+        if not renorm:
+            v = np.array([s[e] for e in chosen])
+        elif score == "softmax":
+            v = np.exp(np.array([x[e] for e in chosen]) - max(x[e] for e in chosen))
+            v = v / v.sum()
+        else:
+            # log sigma(x) = -log(1 + exp(-x)); the ratios hold where sigma underflows
+            lg = np.array([-np.logaddexp(0.0, -x[e]) for e in chosen])
+            v = np.exp(lg - lg.max())
+            v = v / v.sum()
+        w[t, : len(chosen)] = v * scale
+    return ids, w
+
+
+def add_adapters(x, y, ids, a, b, scales, ranks=None):
+    """y + scales[i] b_i (a_i x) per token in fp64 (inputs already fp64)."""
+    out = np.array(y, dtype=np.float64)
+    n, R, _ = a.shape
+    for t, i in enumerate(ids):
+        r = 0 if i < 0 or i >= n else (R if ranks is None else max(0, min(int(ranks[i]), R)))
+        if r:
+            out[t] += float(scales[i]) * (b[i][:, :r] @ (a[i][:r] @ x[t]))
+    return out
+
+
+def block_norm(r, y=None, w_post=None, gate=None, gate_sigmoid=False, w_pre=None, eps=1e-6, branch_scale=1.0,
+               residual_scale=1.0, offset=0.0):
+    """(r', x) in fp64; gate broadcasts against [T, H] (a token gate is [T, 1])."""
+    def norm(v, wt):
+        return v / np.sqrt((v * v).mean(axis=1, keepdims=True) + eps) * (wt + offset)
+
+    r2 = residual_scale * np.asarray(r, dtype=np.float64)
+    if y is not None:
+        u = np.asarray(y, dtype=np.float64)
+        if w_post is not None:
+            u = norm(u, w_post)
+        if gate is not None:
+            u = u * (1.0 / (1.0 + np.exp(-gate)) if gate_sigmoid else gate)
+        r2 = r2 + branch_scale * u
+    return r2, (norm(r2, w_pre) if w_pre is not None else None)
