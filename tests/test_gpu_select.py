@@ -93,6 +93,8 @@ def test_masks(score, G, renorm):
     L[10] = F32_MAX
     L[11] = -3e38
     L[12, 20:] = -np.inf
+    L[13, ::3] = 0.0
+    L[13, 1::3] = -0.0
     bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
     bias[[2, 17, 33]] = [-np.inf, np.nan, -F32_MAX]
     bias[7] = np.inf
