@@ -61,8 +61,10 @@ struct SelectArgs {
     int G, per, keep;       // groups of `per` experts, groups that stay
     bool sigmoid, top2, renorm;
     float scale;
-    int group_lanes_log2;   // set by launch_select: lanes per group, 2^20 / per
+    // set by launch_select: lanes per group, 2^20 / per, floats of a warp's keys
+    int group_lanes_log2;
     unsigned per_magic;
+    int key_room;
 };
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t st);
 

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kSelWarps = 4;         // warps (tokens) of a CTA
 constexpr int kSelCand = 64;         // candidates that a warp's list holds
-constexpr int kSelOneKey = 12;       // up to this k one key per lane sets the threshold
+constexpr int kSelSpare = 4;         // ... and may hold beyond k of the lanes' largest keys
 
 MOE_DEV double warp_sum_d(double v) {
 #pragma unroll
@@ -71,6 +71,22 @@ MOE_DEV void store_weights(const SelectArgs& a, int t, int id, float x, bool on,
     }
 }
 
+// sum of exp(l - top) over the eligible experts in fp64 (softmax)
+MOE_DEV double softmax_total(const SelectArgs& a, const float* row, float top) {
+    double total = 0.0;
+    if (!a.sigmoid)
+        for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+            const float l = __ldg(row + e);
+            if (sel_on(l) && (!a.bias || sel_on(__ldg(a.bias + e)))) total += exp((double)sel_cap(l) - (double)top);
+        }
+    return warp_sum_d(total);
+}
+// (called, not inlined: few tokens come here, and one copy stays in the
+// instruction caches)
+__device__ __noinline__ double exact_score(const SelectArgs& a, double x, float top, double total) {
+    return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / total;
+}
+
 // The whole rule for one token in fp64, one warp, expert e in lane e % 32.
 template <int SLOTS>
 __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
@@ -101,7 +117,7 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
             if (key[i] > -INFINITY) total += exp(key[i] - (double)top);
         total = warp_sum_d(total);
     }
-    auto score = [&](double x) { return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / total; };
+    auto score = [&](double x) { return exact_score(a, x, top, total); };
     const bool scored_groups = a.G > 1 && a.top2 && a.per > 1;
     if (a.bias)
 #pragma unroll 1
@@ -163,6 +179,12 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
     store_weights(a, t, my_id, x, my_on, top, (float)total);
 }
 
+MOE_DEV float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Order-preserving key of a float: larger value, larger key; 0 is below all.
 MOE_DEV uint32_t sel_key(float v) {
     const uint32_t b = __float_as_uint(v + 0.0f);            // -0 counts as +0
@@ -172,15 +194,130 @@ MOE_DEV float sel_value(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 
-// shared memory of one warp
-struct SelScratch {
-    unsigned long long cand[kSelCand];   // candidates: key, then ~expert
-    unsigned long long best[kSelCand];   // by rank
+// shared memory of one warp: the candidates' keys in integer order, their
+// experts, and the candidates by rank
+struct __align__(16) SelScratch {
+    uint32_t key[kSelCand];
+    int expert[kSelCand];
+    int order[kSelCand];
+    double exact[kSelCand];              // fp64 keys, where they are needed
 };
 
-// The rule in fp32 for one token, one warp, expert e in lane e % 32.  false:
-// two keys that matter are too near (or more candidates than there is room
-// for): nothing is written.
+// The candidates ranked by their keys in fp64
+__device__ __noinline__ void rank_exact(const SelectArgs& a, const float* row, float top, int C, SelScratch& sc) {
+    const int lane = threadIdx.x & 31;
+    const double total = softmax_total(a, row, top);
+    double mine[2] = {0.0, 0.0};
+    int e[2] = {0, 0}, rank[2] = {0, 0};
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+        const int j = lane + 32 * u;
+        if (j < C) {
+            e[u] = sc.expert[j];
+            mine[u] = exact_score(a, (double)sel_cap(__ldg(row + e[u])), top, total) + (double)sel_cap(__ldg(a.bias + e[u]));
+            sc.exact[j] = mine[u];
+        }
+    }
+    __syncwarp();
+    for (int j = 0; j < C; ++j) {
+        const double v = sc.exact[j];
+        const int o = sc.expert[j];
+        for (int u = 0; u < 2; ++u) rank[u] += (v > mine[u] || (v == mine[u] && o < e[u])) ? 1 : 0;
+    }
+    for (int u = 0; u < 2; ++u)
+        if (lane + 32 * u < C) sc.order[rank[u]] = lane + 32 * u;
+    __syncwarp();
+}
+
+// The candidates ranked by fp32 key, the lower expert first on equal keys.
+// The keys alone decide unless two are equal: those meet at one rank, and
+// one of them does not find itself there.
+MOE_DEV void rank_fast(int C, SelScratch& sc) {
+    const int lane = threadIdx.x & 31;
+    const bool h0 = lane < C, h1 = lane + 32 < C;
+    const uint32_t k0 = h0 ? sc.key[lane] : 0u, k1 = h1 ? sc.key[lane + 32] : 0u;
+    const uint4* quads = reinterpret_cast<const uint4*>(sc.key);
+    int r0 = 0, r1 = 0;
+    if (C <= 32) {
+        for (int j = 0; j < (C + 3) / 4; ++j) {
+            const uint4 x = quads[j];
+            r0 += (x.x > k0) + (x.y > k0) + (x.z > k0) + (x.w > k0);
+        }
+    } else {
+        for (int j = 0; j < (C + 3) / 4; ++j) {
+            const uint4 x = quads[j];
+            r0 += (x.x > k0) + (x.y > k0) + (x.z > k0) + (x.w > k0);
+            r1 += (x.x > k1) + (x.y > k1) + (x.z > k1) + (x.w > k1);
+        }
+    }
+    if (h0) sc.order[r0] = lane;
+    if (h1) sc.order[r1] = lane + 32;
+    __syncwarp();
+    const bool met = (h0 && sc.order[r0] != lane) || (h1 && sc.order[r1] != lane + 32);
+    if (__any_sync(0xffffffffu, met)) {
+        const int e0 = h0 ? sc.expert[lane] : 0, e1 = h1 ? sc.expert[lane + 32] : 0;
+        for (int j = 0; j < C; ++j) {
+            const uint32_t x = sc.key[j];
+            const int o = sc.expert[j];
+            r0 += x == k0 && o < e0 ? 1 : 0;
+            r1 += x == k1 && o < e1 ? 1 : 0;
+        }
+        if (h0) sc.order[r0] = lane;
+        if (h1) sc.order[r1] = lane + 32;
+        __syncwarp();
+    }
+}
+
+// The rank of the lane's group (lanes as in select_fast) by fp64 scores; -1:
+// too many members to list.  Only members whose fp32 key reaches their group's
+// second largest (largest: max scores), less both errors, can be among its two
+// largest keys: they are listed first, so that the lanes take their fp64 keys
+// side by side.
+__device__ __noinline__ int group_rank_exact(const SelectArgs& a, const float* row, float top, const float* gkey, float b1, float b2,
+                                             float ks, SelScratch& sc) {
+    const int lane = threadIdx.x & 31;
+    const unsigned all = 0xffffffffu;
+    const int gl = a.group_lanes_log2, g = lane >> gl, L = 1 << gl;
+    const double total = softmax_total(a, row, top);
+    const bool top2 = a.top2 && a.per > 1;
+    const float last = top2 && b2 > -INFINITY ? b2 : b1;
+    const float bar = last - (2.1f * ks + 3e-7f * fabsf(last));
+    int n = 0;
+    for (int j0 = 0; j0 < a.per; j0 += L) {
+        const int j = j0 + (lane & (L - 1)), e = g * a.per + j;
+        const bool hit = g < a.G && j < a.per && gkey[e] > -INFINITY && gkey[e] >= bar;
+        const unsigned who = __ballot_sync(all, hit);
+        const int p = n + __popc(who & ((1u << lane) - 1u));
+        n += __popc(who);
+        if (n > kSelCand) return -1;
+        if (hit) { sc.expert[p] = e; sc.order[p] = g; }
+    }
+    __syncwarp();
+    for (int j = lane; j < n; j += 32)
+        sc.exact[j] = exact_score(a, (double)sel_cap(__ldg(row + sc.expert[j])), top, total) + (a.bias ? (double)sel_cap(__ldg(a.bias + sc.expert[j])) : 0.0);
+    __syncwarp();
+    double d1 = -INFINITY, d2 = -INFINITY;
+    for (int j = 0; j < n; ++j)
+        if (sc.order[j] == g) {
+            const double x = sc.exact[j];
+            d2 = fmax(d2, fmin(d1, x));
+            d1 = fmax(d1, x);
+        }
+    __syncwarp();
+    const double mine = top2 && d2 > -INFINITY ? d1 + d2 : d1;
+    int rank = 0;
+    for (int q = 0; q < a.G; ++q) {
+        const double x = __shfl_sync(all, mine, q << gl);
+        rank += (x > mine || (x == mine && q < g)) ? 1 : 0;
+    }
+    return rank;
+}
+
+// The rule in fp32 for one token, one warp; lane l holds the experts
+// 128 i + 4 ((l + 9 i) % 32) + q in v[4 i + q] (turned from chunk to chunk, so
+// that the groups that stay are not all in a few lanes).  Group scores, and then keys, that are nearer
+// than their errors are taken again in fp64.  false: the candidates are more
+// than the list holds, or fewer than k; nothing is written.
 //
 // Error bounds.  ks: of a score.  sigmoid: __expf is off by 2 + 1.173 |x| ulp,
 // which the score sees as at most (4 + 0.37 x 2.4) x 2^-24 absolute, plus 3 ulp
@@ -190,88 +327,110 @@ struct SelScratch {
 // top - x under the softmax is at most ln 1024): 3.5e-6 / S; 5e-6 / S is taken.
 // A key adds half a step, 2^-24 of its size.
 //
-// Threshold: each lane's M largest keys; t is reached by at least k of them, so
-// no key below t (less both errors) is among the k best.  t comes from bisecting
-// the keys' integer order by ballots, until it is reached by k to k + 2 of them:
-// about 12 candidates of 512 for k = 10.  M = 2 for k > 12, where one key per
-// lane would leave far more candidates than k (130 for k = 32).  Candidates go
-// to the warp's list and each is ranked by counting those ahead of it.
-template <int SLOTS>
+// Threshold: each lane's two largest keys; t is reached by at least k of them,
+// so no key below t (less both errors) is among the k best.  t comes from
+// bisecting the keys' integer order by ballots, until it is reached by k to
+// k + 4 of them: about 15 candidates of 512 for k = 10 and 40 of 1024 for
+// k = 32 (one key per lane would leave 130 there).  The candidates go to the
+// warp's list and each is ranked by counting those ahead of it.
+template <int CH, bool VEC>
 MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey) {
+    constexpr int SLOTS = 4 * CH;
     const int lane = threadIdx.x & 31;
     const unsigned all = 0xffffffffu;
     const float* row = a.logits + (size_t)t * a.ld;
-    float x[SLOTS];
+    auto first = [&](int i) { return 128 * i + 4 * ((lane + 9 * i) & 31); };
+    // four consecutive floats from p[e], off: what stands for entries past E
+    auto load4 = [&](const float* p, int e, float off, float* d) {
+        if (VEC) {
+            const float4 q = e < a.E ? __ldg(reinterpret_cast<const float4*>(p + e)) : make_float4(off, off, off, off);
+            d[0] = q.x; d[1] = q.y; d[2] = q.z; d[3] = q.w;
+        } else {
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
-        const int e = lane + 32 * i;
-        x[i] = e < a.E ? __ldg(row + e) : -FLT_MAX;
-    }
-    uint32_t on = 0;
-    float top = -FLT_MAX;
+            for (int q = 0; q < 4; ++q) d[q] = e + q < a.E ? __ldg(p + e + q) : off;
+        }
+    };
+    float v[SLOTS];                                  // eligible: above -FLT_MAX
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
-        bool ok = sel_on(x[i]);
-        x[i] = sel_cap(x[i]);
-        if (a.bias && lane + 32 * i < a.E) ok = ok && sel_on(__ldg(a.bias + lane + 32 * i));
-        on |= ok ? 1u << i : 0u;
-        if (ok) top = fmaxf(top, x[i]);
-    }
-    if (!__any_sync(all, on != 0)) {                 // nothing eligible: experts 0 .. k-1, weights 0
-        store_weights(a, t, lane, 0.0f, false, 0.0f, 1.0f);
-        return true;
-    }
+    for (int i = 0; i < CH; ++i) load4(row, first(i), -FLT_MAX, v + 4 * i);
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) v[i] = fmaxf(v[i], -FLT_MAX);        // NaN and -inf too
     const bool top2 = a.G > 1 && a.top2 && a.per > 1;
     const bool scored = a.bias != nullptr || top2;   // keys or group scores need the scores
-    float total = 1.0f, ks = 1e-6f;
+    float top = -FLT_MAX, total = 1.0f, ks = 1e-6f;
     if (!a.sigmoid && (scored || !a.renorm)) {
-        top = warp_max(top);
         float s = 0.0f;
+        if (a.bias) {                                // experts that their bias switches off leave the softmax
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i)
-            if ((on >> i) & 1u) s += expf(x[i] - top);
+            for (int i = 0; i < CH; ++i) {
+                float b[4];
+                load4(a.bias, first(i), -FLT_MAX, b);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[4 * i + q] = sel_on(b[q]) ? v[4 * i + q] : -FLT_MAX;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) top = fmaxf(top, v[i]);
+        top = fminf(warp_max(top), FLT_MAX);
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) s += sel_on(v[i]) ? expf(sel_cap(v[i]) - top) : 0.0f;
         total = warp_sum(s);
         ks = __fdividef(5e-6f, total);
     }
-    uint32_t key[SLOTS];                             // 0: not eligible
-    if (scored) {
+    if (scored || a.G > 1) {
         const float inv = __fdividef(1.0f, total);
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-            const int e = lane + 32 * i;
-            const bool ok = (on >> i) & 1u;
-            float v = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : expf(x[i] - top) * inv;
-            if (a.bias) v += ok ? sel_cap(__ldg(a.bias + e)) : 0.0f;
-            if (a.G > 1 && e < a.E) gkey[e] = ok ? v : -INFINITY;
-            key[i] = ok ? sel_key(a.bias ? v : x[i]) : 0u;
-        }
-    } else {
+        for (int i = 0; i < CH; ++i) {
+            const int e = first(i);
+            float b[4] = {0.0f, 0.0f, 0.0f, 0.0f}, g[4];
+            if (a.bias) load4(a.bias, e, -FLT_MAX, b);
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-            const int e = lane + 32 * i;
-            const bool ok = (on >> i) & 1u;
-            if (a.G > 1 && e < a.E) gkey[e] = ok ? x[i] : -INFINITY;
-            key[i] = ok ? sel_key(x[i]) : 0u;
+            for (int q = 0; q < 4; ++q) {
+                float& x = v[4 * i + q];
+                float key = sel_cap(x);
+                if (scored) key = a.sigmoid ? rcp_approx(1.0f + __expf(-x)) : expf(key - top) * inv;
+                if (a.bias) key += sel_cap(b[q]);
+                g[q] = sel_on(x) && sel_on(b[q]) ? key : -INFINITY;
+                if (a.bias) x = g[q];
+            }
+            if (VEC) {
+                if (e < a.E) *reinterpret_cast<float4*>(gkey + e) = make_float4(g[0], g[1], g[2], g[3]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (e + q < a.E) gkey[e + q] = g[q];
+            }
         }
+        __syncwarp();
     }
     if (a.G > 1) {
         // 2^gl lanes per group, their largest two keys folded together; each
         // group starts at another offset so that the lanes' banks differ
         const int gl = a.group_lanes_log2, L = 1 << gl;
         const int g = lane >> gl, sub = lane & (L - 1);
-        const int nit = (a.per + L - 1) >> gl;
-        __syncwarp();
         float b1 = -INFINITY, b2 = -INFINITY;
+        auto take = [&](float x) {
+            b2 = fmaxf(b2, fminf(b1, x));
+            b1 = fmaxf(b1, x);
+        };
         if (g < a.G) {
+            const bool quads = VEC && (a.per & 3) == 0;
+            const int m = quads ? a.per >> 2 : a.per, nit = (m + L - 1) >> gl;
             int it = g % nit;
             for (int n = 0; n < nit; ++n) {
                 const int j = sub + (it << gl);
-                const float v = j < a.per ? gkey[g * a.per + j] : -INFINITY;
-                b2 = fmaxf(b2, fminf(b1, v));
-                b1 = fmaxf(b1, v);
+                if (j < m) {
+                    if (quads) {
+                        const float4 x = *reinterpret_cast<const float4*>(gkey + g * a.per + 4 * j);
+                        take(x.x); take(x.y); take(x.z); take(x.w);
+                    } else {
+                        take(gkey[g * a.per + j]);
+                    }
+                }
                 it = it + 1 == nit ? 0 : it + 1;
             }
         }
+        __syncwarp();
         for (int o = L >> 1; o > 0; o >>= 1) {
             const float c1 = __shfl_xor_sync(all, b1, o), c2 = __shfl_xor_sync(all, b2, o);
             b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
@@ -281,8 +440,8 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
         // rank of this lane's group: lane g << gl speaks for group g
         int rank = 0;
         for (int q = 0; q < a.G; ++q) {
-            const float v = __shfl_sync(all, mine, q << gl);
-            rank += (v > mine || (v == mine && q < g)) ? 1 : 0;
+            const float x = __shfl_sync(all, mine, q << gl);
+            rank += (x > mine || (x == mine && q < g)) ? 1 : 0;
         }
         const bool speaks = g < a.G && sub == 0;
         if (scored && a.keep < a.G) {
@@ -291,53 +450,61 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
             const float big = warp_max(speaks && mine > -INFINITY ? fmaxf(fabsf(b1), fabsf(mine)) : 0.0f);
             const float in = warp_max(speaks && rank == a.keep - 1 ? mine : -INFINITY);
             const float out = warp_max(speaks && rank == a.keep ? mine : -INFINITY);
-            if (out > -INFINITY && !(in - out > 4.2f * ks + 7.5e-7f * big)) return false;
+            if (out > -INFINITY && !(in - out > 4.2f * ks + 7.5e-7f * big)) {
+                rank = group_rank_exact(a, row, top, gkey, b1, b2, ks, sc);
+                if (rank < 0) return false;
+            }
         }
-        const unsigned speak = __ballot_sync(all, speaks && rank < a.keep);
+        const unsigned kept = __ballot_sync(all, speaks && rank < a.keep);
+        auto stays = [&](int e) { return (kept >> (((((unsigned)e * a.per_magic) >> 20) << gl) & 31u)) & 1u; };
+        if ((a.per & 3) == 0) {                      // four neighbours share their group
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-            const unsigned ge = ((unsigned)(lane + 32 * i) * a.per_magic) >> 20;      // e / per
-            if (!((speak >> ((ge << gl) & 31u)) & 1u)) key[i] = 0u;
+            for (int i = 0; i < CH; ++i)
+                if (!stays(first(i))) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[4 * i + q] = -FLT_MAX;
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                if (!stays(first(i / 4) + (i & 3))) v[i] = -FLT_MAX;
         }
-        __syncwarp();
     }
-    // the lane's largest keys
-    uint32_t m1 = 0, m2 = 0;
+    // the lane's largest keys in their integer order, 0 for none
+    float f1 = -FLT_MAX, f2 = -FLT_MAX;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-        m2 = max(m2, min(m1, key[i]));
-        m1 = max(m1, key[i]);
+        f2 = fmaxf(f2, fminf(f1, v[i]));
+        f1 = fmaxf(f1, v[i]);
     }
-    if (a.k <= kSelOneKey) m2 = 0;
-    uint32_t lo = __reduce_min_sync(all, m1), hi = __reduce_max_sync(all, m1);
-    if (hi == 0) {                                   // no eligible expert in the groups that stay
-        return false;
+    const uint32_t m1 = sel_on(f1) ? sel_key(sel_cap(f1)) : 0u, m2 = sel_on(f2) ? sel_key(sel_cap(f2)) : 0u;
+    uint32_t lo = max(__reduce_min_sync(all, m1), 1u), hi = __reduce_max_sync(all, m1);
+    if (hi == 0) {                                   // nothing eligible: experts 0 .. k-1, weights 0
+        store_weights(a, t, lane, 0.0f, false, 0.0f, 1.0f);
+        return true;
     }
-    if (lo == 0) lo = 1;
-    auto reached = [&](uint32_t v) { return __popc(__ballot_sync(all, m1 >= v)) + __popc(__ballot_sync(all, m2 >= v)); };
-    if (reached(lo) < a.k) {
-        lo = 1;                                      // few lanes hold keys: every eligible expert
-    } else {
+    auto reached = [&](uint32_t x) { return __popc(__ballot_sync(all, m1 >= x)) + __popc(__ballot_sync(all, m2 >= x)); };
+    const float lowest = sel_value(sel_key(-FLT_MAX) + 1u);
+    float bar = lowest;                              // few lanes hold keys: every eligible expert
+    if (reached(lo) >= a.k) {
         while (hi - lo > 1) {
             const uint32_t mid = lo + ((hi - lo) >> 1);
             const int c = reached(mid);
             if (c >= a.k) {
                 lo = mid;
-                if (c <= a.k + 2) break;
+                if (c <= a.k + kSelSpare) break;
             } else {
                 hi = mid;
             }
         }
-    }
-    if (a.bias && lo > 1) {
-        const float v = sel_value(lo);
-        lo = max(1u, sel_key(v - (2.1f * ks + 3e-7f * fabsf(v))));
+        bar = fmaxf(sel_value(lo), lowest);
+        if (a.bias) bar = fmaxf(bar - (2.1f * ks + 3e-7f * fabsf(bar)), lowest);
     }
     unsigned cm = 0;
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) cm |= key[i] >= lo ? 1u << i : 0u;
-    const int mineN = __popc(cm);
-    int incl = mineN;
+    for (int i = 0; i < SLOTS; ++i) cm |= v[i] >= bar ? 1u << i : 0u;
+    const int n = __popc(cm);
+    int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(all, incl, o);
@@ -345,58 +512,56 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
     }
     const int C = __shfl_sync(all, incl, 31);
     if (C > kSelCand || C < a.k) return false;
-    {
-        int p = incl - mineN;
-#pragma unroll
-        for (int i = 0; i < SLOTS; ++i)
-            if ((cm >> i) & 1u) sc.cand[p++] = ((unsigned long long)key[i] << 32) | (uint32_t)~(lane + 32 * i);
+    for (int p = incl - n; cm; cm &= cm - 1) {
+        const int i = __ffs(cm) - 1;
+        sc.expert[p++] = first(i >> 2) + (i & 3);
     }
     __syncwarp();
-    {
-        const unsigned long long c0 = lane < C ? sc.cand[lane] : 0ull, c1 = lane + 32 < C ? sc.cand[lane + 32] : 0ull;
-        int r0 = 0, r1 = 0;
-        if (C <= 32) {
-            for (int j = 0; j < C; ++j) r0 += sc.cand[j] > c0 ? 1 : 0;
-        } else {
-            for (int j = 0; j < C; ++j) {
-                const unsigned long long v = sc.cand[j];
-                r0 += v > c0 ? 1 : 0;
-                r1 += v > c1 ? 1 : 0;
-            }
-        }
-        if (lane < C) sc.best[r0] = c0;
-        if (lane + 32 < C) sc.best[r1] = c1;
-    }
+    // the last four are filled up with 0, which is behind all
+    for (int j = lane; j < ((C + 3) & ~3); j += 32)
+        sc.key[j] = j < C ? sel_key(a.bias ? gkey[sc.expert[j]] : sel_cap(__ldg(row + sc.expert[j]))) : 0u;
     __syncwarp();
-    const unsigned long long me = lane < a.k ? sc.best[lane] : 0ull;
-    const int id = (int)~(uint32_t)me;
-    float xs = 0.0f;
-    if (lane < a.k) xs = sel_cap(__ldg(row + id));
+    rank_fast(C, sc);
     if (a.bias) {
+        // neighbours in the order, and the k-th against the next one
         bool near = false;
         if (lane < a.k && lane + 1 < C) {
-            const unsigned long long nx = sc.best[lane + 1];
-            const float v = sel_value((uint32_t)(me >> 32)), u = sel_value((uint32_t)(nx >> 32));
-            if (!(v - u > 2.0f * ks + 2.4e-7f * fmaxf(fabsf(v), fabsf(u)))) {
+            const int j1 = sc.order[lane], j2 = sc.order[lane + 1];
+            const float x = sel_value(sc.key[j1]), y = sel_value(sc.key[j2]);
+            if (!(x - y > 2.0f * ks + 2.4e-7f * fmaxf(fabsf(x), fabsf(y)))) {
                 // equal logits and biases are equal keys: the lower expert first
-                const int e2 = (int)~(uint32_t)nx;
-                near = !(xs == sel_cap(__ldg(row + e2)) && sel_cap(__ldg(a.bias + id)) == sel_cap(__ldg(a.bias + e2)));
+                const int e1 = sc.expert[j1], e2 = sc.expert[j2];
+                near = !(sel_cap(__ldg(row + e1)) == sel_cap(__ldg(row + e2)) && sel_cap(__ldg(a.bias + e1)) == sel_cap(__ldg(a.bias + e2)));
             }
         }
-        if (__any_sync(all, near)) return false;
+        if (__any_sync(all, near)) rank_exact(a, row, top, C, sc);
     }
+    const int j = lane < a.k ? sc.order[lane] : 0;
+    const int id = sc.expert[j];
+    const float xs = lane < a.k ? (a.bias ? sel_cap(__ldg(row + id)) : sel_value(sc.key[j])) : 0.0f;
     store_weights(a, t, id, xs, true, top, total);
     return true;
 }
 
-template <int SLOTS>
-__global__ void __launch_bounds__(kSelWarps * 32, SLOTS == 32 ? 6 : 8) k_select(SelectArgs a) {
+template <int CH, bool VEC>
+__global__ void __launch_bounds__(kSelWarps * 32, CH == 8 ? 6 : 8) k_select(const __grid_constant__ SelectArgs a) {
     __shared__ SelScratch scratch[kSelWarps];
-    extern __shared__ float gkeys[];                 // [kSelWarps][E] with groups
+    extern __shared__ __align__(16) float gkeys[];   // [kSelWarps][key_room] with groups or a bias
     const int w = threadIdx.x >> 5;
     const int t = blockIdx.x * kSelWarps + w;
     if (t >= a.T) return;
-    if (!select_fast<SLOTS>(a, t, scratch[w], gkeys + (size_t)w * a.E)) select_exact<SLOTS>(a, t);
+    if (!select_fast<CH, VEC>(a, t, scratch[w], gkeys + w * a.key_room)) select_exact<4 * CH>(a, t);
+}
+
+template <int CH>
+void launch_ch(const SelectArgs& a, cudaStream_t st) {
+    const unsigned grid = (unsigned)((a.T + kSelWarps - 1) / kSelWarps);
+    const size_t smem = a.G > 1 || a.bias ? sizeof(float) * kSelWarps * (size_t)a.key_room : 0;
+    // rows of whole, aligned 16-byte vectors
+    const bool vec = a.E % 4 == 0 && (a.T == 1 || a.ld % 4 == 0) && (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0;
+    if (vec) k_select<CH, true><<<grid, kSelWarps * 32, smem, st>>>(a);
+    else k_select<CH, false><<<grid, kSelWarps * 32, smem, st>>>(a);
 }
 
 }  // namespace
@@ -406,11 +571,10 @@ cudaError_t launch_select(const SelectArgs& args, cudaStream_t st) {
     a.group_lanes_log2 = 0;
     while (a.G > 1 && (a.G << (a.group_lanes_log2 + 1)) <= 32) ++a.group_lanes_log2;
     a.per_magic = ((1u << 20) + a.per - 1) / a.per;  // e * magic >> 20 = e / per for e, per <= 1024
-    const unsigned grid = (unsigned)((a.T + kSelWarps - 1) / kSelWarps);
-    const size_t smem = a.G > 1 ? sizeof(float) * kSelWarps * (size_t)a.E : 0;
-    if (a.E <= 256) k_select<8><<<grid, kSelWarps * 32, smem, st>>>(a);
-    else if (a.E <= 512) k_select<16><<<grid, kSelWarps * 32, smem, st>>>(a);
-    else k_select<32><<<grid, kSelWarps * 32, smem, st>>>(a);
+    a.key_room = (a.E + 3) & ~3;
+    if (a.E <= 256) launch_ch<2>(a, st);
+    else if (a.E <= 512) launch_ch<4>(a, st);
+    else launch_ch<8>(a, st);
     return cudaGetLastError();
 }
 
