@@ -18,6 +18,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+constexpr int kAdTokenMax = 64;      // up to this T a cluster per token
+constexpr int kAdSmallTile = 2048;   // up to this T tiles of 16 tokens, then of 64
 constexpr int kAdThreads = 256;
 constexpr int kAdCluster = 8;
 
@@ -31,7 +33,7 @@ MOE_DEV float dot8(const uint4& p, const uint4& q, float s) {
     return s;
 }
 
-__global__ void __launch_bounds__(kAdThreads) k_adapter_token(AdapterArgs a) {
+__global__ void __launch_bounds__(kAdThreads) k_adapter_token(const __grid_constant__ AdapterArgs a) {
     __shared__ float part[kAdapterMaxRank];      // this CTA's share of z
     __shared__ float z[kAdapterMaxRank];
     cg::cluster_group cl = cg::this_cluster();
@@ -83,9 +85,302 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_token(AdapterArgs a) {
     }
 }
 
+// D (16 x 8, fp32) += A (16 x 16, bf16) B (16 x 8, bf16)
+MOE_DEV void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Many tokens: a cluster of kTileCluster CTAs takes BT = 16 MT MG consecutive
+// tokens.  Both products run on mma.sync m16n8k16 straight from global memory.
+//
+//   1. z = A_i x: the cluster's 8 / MG x kTileCluster column shares of x, a warp
+//      per share and 16 MT rows; the shares meet in shared memory, then across
+//      the cluster.  A warp repeats this for each adapter among its rows and
+//      keeps each row's own.
+//   2. out = y + B_i (scale z): the same split over the N outputs.
+//
+// Fragments.  A sum over k may take k in any order, so lane (g, c) (g = lane / 4,
+// c = lane % 4) loads 16 bytes, columns 8c .. 8c+7 of a 32-column chunk, from
+// row g of either operand: words 0, 1 are its k pairs of the chunk's first
+// mma, words 2, 3 of the second.  Likewise column 2c + i of the n-tile j of a
+// group of four stands for 8c + 2j + i, so that a lane's results of the four
+// tiles are eight neighbours (16-byte loads of y and stores of out), and z's
+// results are, without any exchange, the first operand of step 2 with B's
+// 16-byte loads.
+//
+// RG: groups of 32 rank rows.  WIDE: y and out fp32; z is then held as two bf16
+// halves (16 significant bits), as one otherwise.
+constexpr int kTileCluster = 4;
+constexpr int kTileWarps = 8;
+
+template <int RG, int MT, int MG>
+constexpr size_t tile_smem_bytes() {
+    // [parts][MG][MT][4 RG tiles][2 row halves][32 lanes] float2
+    return (size_t)(kTileWarps / MG) * MG * MT * 4 * RG * 2 * 32 * sizeof(float2);
+}
+
+template <int RG, int MT, int MG, bool WIDE>
+__global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_tile(const __grid_constant__ AdapterArgs a) {
+    constexpr int BT = 16 * MT * MG, PARTS = kTileWarps / MG, TJ = 4 * RG, NPASS = RG == 4 ? 2 : 1, PJ = TJ / NPASS;
+    constexpr int ZN = MG * MT * TJ * 2 * 32;             // float2 values of z
+    extern __shared__ __align__(16) float2 part_s[];      // [PARTS][ZN]; later zf in place of part 1 on
+    __shared__ float s_scale[BT];
+    cg::cluster_group cl = cg::this_cluster();
+    const int crank = (int)cl.block_rank();
+    const int t0 = (int)(blockIdx.x / kTileCluster) * BT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int mg = warp % MG, part = warp / MG;
+    const int r0 = t0 + 16 * MT * mg;                     // the warp's first row
+    auto rank_of = [&](int id) { return min(a.ranks ? __ldg(a.ranks + id) : a.R, a.R); };
+    // the adapters of the warp's rows (lane: row), -1 for none
+    int myid = -1;
+    if (lane < 16 * MT && r0 + lane < a.T) {
+        const int id = __ldg(a.ids + r0 + lane);
+        if (id >= 0 && id < a.n && rank_of(id) > 0) myid = id;
+    }
+    if (part == 0 && lane < 16 * MT) s_scale[16 * MT * mg + lane] = myid >= 0 ? __ldg(a.scales + myid) : 0.0f;
+    const unsigned with = __ballot_sync(0xffffffffu, myid >= 0);
+    const int share = crank * PARTS + part;
+    constexpr int SHARES = kTileCluster * PARTS;
+    {
+        // ------------------------------------------------ z, this warp's columns
+        const int nch = (a.K + 31) / 32;
+        const int lo = (int)((long long)nch * share / SHARES), hi = (int)((long long)nch * (share + 1) / SHARES);
+        float2* mine = part_s + (size_t)part * ZN + mg * (MT * TJ * 2 * 32) + lane;
+        const __nv_bfloat16* xr[2 * MT];
+#pragma unroll
+        for (int u = 0; u < 2 * MT; ++u)
+            xr[u] = reinterpret_cast<const __nv_bfloat16*>(a.x) + (size_t)min(r0 + g + 8 * u, a.T - 1) * a.ld_x + 8 * c;
+        if (with == 0) {
+#pragma unroll
+            for (int i = 0; i < MT * TJ * 2; ++i) mine[i * 32] = make_float2(0.0f, 0.0f);
+        }
+        for (unsigned todo = with; todo;) {
+            const int id = __shfl_sync(0xffffffffu, myid, __ffs(todo) - 1);
+            const unsigned mem = __ballot_sync(0xffffffffu, myid == id);
+            const bool first = todo == with;
+            todo &= ~mem;
+            const int rk = rank_of(id);
+            const __nv_bfloat16* arow = reinterpret_cast<const __nv_bfloat16*>(a.a) + ((size_t)id * a.R + 8 * (g >> 1) + (g & 1)) * a.K + 8 * c;
+#pragma unroll 1
+            for (int p = 0; p < NPASS; ++p) {
+                float acc[MT][PJ][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < PJ; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[m][j][q] = 0.0f;
+#pragma unroll 2
+                for (int ch = lo; ch < hi; ++ch) {
+                    const bool in = 32 * ch + 8 * c < a.K;
+                    uint4 xv[2 * MT], av[PJ];
+#pragma unroll
+                    for (int u = 0; u < 2 * MT; ++u) xv[u] = in ? ldg_stream_v4(xr[u] + 32 * ch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < PJ; ++j) {
+                        const int ro = 32 * (j / 4) + 2 * (j & 3) + 32 * (PJ / 4) * p;    // row: ro + 8 (g / 2) + g % 2
+                        av[j] = in && ro + 8 * (g >> 1) + (g & 1) < rk ? ldg_nc_v4(arow + (size_t)ro * a.K + 32 * ch) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int j = 0; j < PJ; ++j)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            mma_16816(acc[m][j], xv[2 * m].x, xv[2 * m + 1].x, xv[2 * m].y, xv[2 * m + 1].y, av[j].x, av[j].y);
+                            mma_16816(acc[m][j], xv[2 * m].z, xv[2 * m + 1].z, xv[2 * m].w, xv[2 * m + 1].w, av[j].z, av[j].w);
+                        }
+                }
+                // each row's own adapter; rows without one get zeros
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bool own = (mem >> (16 * m + 8 * h + g)) & 1u;
+                        const bool none = !((with >> (16 * m + 8 * h + g)) & 1u);
+                        if (own || (first && none)) {
+#pragma unroll
+                            for (int j = 0; j < PJ; ++j)
+                                mine[((m * TJ + PJ * p + j) * 2 + h) * 32] = own ? make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1])
+                                                                                 : make_float2(0.0f, 0.0f);
+                        }
+                    }
+            }
+        }
+    }
+    __syncthreads();
+    // ------------------------------------- the CTA's shares, then the cluster's
+    for (int i = threadIdx.x; i < ZN; i += kTileWarps * 32) {
+        float2 v = part_s[i];
+#pragma unroll
+        for (int q = 1; q < PARTS; ++q) {
+            const float2 o = part_s[(size_t)q * ZN + i];
+            v.x += o.x;
+            v.y += o.y;
+        }
+        part_s[i] = v;
+    }
+    cl.sync();
+    // z * scale as the second product's first operand: [MG][MT][2 RG steps][32
+    // lanes][4 words], for WIDE the low halves behind it
+    uint32_t* zf = reinterpret_cast<uint32_t*>(part_s + ZN);
+    for (int i = threadIdx.x; i < ZN; i += kTileWarps * 32) {
+        float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int q = 0; q < kTileCluster; ++q) {
+            const float2 o = cl.map_shared_rank(part_s, q)[i];
+            v.x += o.x;
+            v.y += o.y;
+        }
+        const int l = i & 31, h = (i >> 5) & 1, j = (i >> 6) % TJ, mm = (i >> 6) / TJ;     // mm: 16-row tile of the block
+        const float sc = s_scale[16 * mm + 8 * h + (l >> 2)];
+        v.x *= sc;
+        v.y *= sc;
+        const uint32_t hi = pack_bf16x2(v.x, v.y);
+        const int w = ((mm * 2 * RG + (j >> 1)) * 32 + l) * 4 + (j & 1) * 2 + h;
+        zf[w] = hi;
+        if (WIDE) zf[ZN + w] = pack_bf16x2(v.x - bf16_lo(hi), v.y - bf16_hi(hi));
+    }
+    // the others may still read this CTA's sums: waited for at the end
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    __syncthreads();
+    {
+        // ------------------------------------------- out, this warp's columns
+        const int ng = (a.N + 31) / 32;
+        const int lo = (int)((long long)ng * share / SHARES), hi = (int)((long long)ng * (share + 1) / SHARES);
+        const uint4* zq = reinterpret_cast<const uint4*>(zf) + (size_t)(mg * MT) * 2 * RG * 32 + lane;
+        for (int cgp = lo; cgp < hi; ++cgp) {
+            const int col = 32 * cgp + 8 * c;                         // this lane's eight outputs
+            float delta[MT][4][4];
+            uint4 yv[2 * MT][WIDE ? 2 : 1];
+#pragma unroll
+            for (int u = 0; u < 2 * MT; ++u) {
+                const bool in = r0 + g + 8 * u < a.T && col < a.N;
+                const size_t off = (size_t)(r0 + g + 8 * u) * a.ld_y + col;
+                if (WIDE) {
+                    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(a.y) + off);
+                    yv[u][0] = in ? p[0] : make_uint4(0, 0, 0, 0);
+                    yv[u][WIDE ? 1 : 0] = in ? p[1] : make_uint4(0, 0, 0, 0);
+                } else {
+                    yv[u][0] = in ? *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.y) + off) : make_uint4(0, 0, 0, 0);
+                }
+            }
+            for (unsigned todo = with; todo;) {
+                const int id = __shfl_sync(0xffffffffu, myid, __ffs(todo) - 1);
+                const unsigned mem = __ballot_sync(0xffffffffu, myid == id);
+                todo &= ~mem;
+                const int rk = rank_of(id);
+                float acc[MT][4][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[m][j][q] = 0.0f;
+#pragma unroll
+                for (int G = 0; G < RG; ++G) {
+                    const int left = rk - (32 * G + 8 * c);           // columns of this lane's eight in use
+                    uint4 bv[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int n = 32 * cgp + 8 * (g >> 1) + 2 * j + (g & 1);
+                        bv[j] = left > 0 && n < a.N ? ldg_nc_v4(reinterpret_cast<const __nv_bfloat16*>(a.b) + ((size_t)id * a.N + n) * a.R + 32 * G + 8 * c)
+                                                    : make_uint4(0, 0, 0, 0);
+                        if (left > 0 && left < 8) {
+                            uint32_t* wd = &bv[j].x;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) wd[q] &= left >= 2 * q + 2 ? 0xffffffffu : (left == 2 * q + 1 ? 0xffffu : 0u);
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int lowhalf = 0; lowhalf < (WIDE ? 2 : 1); ++lowhalf) {
+                            const uint4* zp = zq + (size_t)(m * 2 * RG + 2 * G) * 32 + lowhalf * (ZN / 4);
+                            const uint4 z0 = zp[0], z1 = zp[32];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                mma_16816(acc[m][j], z0.x, z0.y, z0.z, z0.w, bv[j].x, bv[j].y);
+                                mma_16816(acc[m][j], z1.x, z1.y, z1.z, z1.w, bv[j].z, bv[j].w);
+                            }
+                        }
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if ((mem >> (16 * m + 8 * h + g)) & 1u) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                delta[m][j][2 * h] = acc[m][j][2 * h];
+                                delta[m][j][2 * h + 1] = acc[m][j][2 * h + 1];
+                            }
+                        }
+            }
+#pragma unroll
+            for (int u = 0; u < 2 * MT; ++u) {
+                if (r0 + g + 8 * u >= a.T || col >= a.N) continue;
+                const int m = u >> 1, h = u & 1;
+                const bool own = (with >> (8 * u + g)) & 1u;          // rows without an adapter keep y's bits
+                const size_t off = (size_t)(r0 + g + 8 * u) * a.ld_out + col;
+                uint32_t* y = &yv[u][0].x;
+                if (WIDE) {
+                    uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<float*>(a.out) + off);
+                    uint32_t* y1 = &yv[u][WIDE ? 1 : 0].x;
+                    if (own) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            y[q] = __float_as_uint(__uint_as_float(y[q]) + delta[m][q >> 1][2 * h + (q & 1)]);
+                            y1[q] = __float_as_uint(__uint_as_float(y1[q]) + delta[m][2 + (q >> 1)][2 * h + (q & 1)]);
+                        }
+                    }
+                    p[0] = yv[u][0];
+                    p[1] = yv[u][WIDE ? 1 : 0];
+                } else {
+                    if (own) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) y[j] = pack_bf16x2(bf16_lo(y[j]) + delta[m][j][2 * h], bf16_hi(y[j]) + delta[m][j][2 * h + 1]);
+                    }
+                    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + off) = yv[u][0];
+                }
+            }
+        }
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int RG, int MT, int MG, bool WIDE>
+cudaError_t launch_tile(const AdapterArgs& a, cudaStream_t st) {
+    constexpr int BT = 16 * MT * MG;
+    constexpr size_t smem = tile_smem_bytes<RG, MT, MG>();
+    cudaError_t e = cudaFuncSetAttribute(k_adapter_tile<RG, MT, MG, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((a.T + BT - 1) / BT) * kTileCluster);
+    cfg.blockDim = dim3(kTileWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kTileCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_adapter_tile<RG, MT, MG, WIDE>, a);
+}
+
+template <int MT, int MG>
+cudaError_t launch_tiles(const AdapterArgs& a, cudaStream_t st) {
+    if (a.R <= 32) return a.wide ? launch_tile<1, MT, MG, true>(a, st) : launch_tile<1, MT, MG, false>(a, st);
+    if (a.R <= 64) return a.wide ? launch_tile<2, MT, MG, true>(a, st) : launch_tile<2, MT, MG, false>(a, st);
+    return a.wide ? launch_tile<4, MT, MG, true>(a, st) : launch_tile<4, MT, MG, false>(a, st);
+}
+
 }  // namespace
 
 cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st) {
+    if (a.T > kAdTokenMax) return a.T > kAdSmallTile ? launch_tiles<2, 2>(a, st) : launch_tiles<1, 1>(a, st);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.T * kAdCluster);
     cfg.blockDim = dim3(kAdThreads);

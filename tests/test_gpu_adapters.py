@@ -51,7 +51,8 @@ def assert_close(out, d, ids, ranks=None):
 
 
 SHAPES = [(1, 2048, 2048, 16, 3), (1, 8, 8, 8, 1), (2, 72, 40, 24, 2), (7, 256, 512, 128, 4), (16, 512, 264, 40, 5), (17, 520, 1000, 8, 3),
-          (61, 1024, 512, 32, 40), (130, 264, 136, 64, 6), (200, 2048, 256, 16, 11), (333, 136, 72, 56, 2)]
+          (61, 1024, 512, 32, 40), (130, 264, 136, 64, 6), (200, 2048, 256, 16, 11), (333, 136, 72, 56, 2),
+          (2113, 136, 72, 24, 7), (2305, 64, 96, 64, 30), (2200, 72, 40, 128, 3), (2049, 520, 264, 96, 4)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -69,7 +70,7 @@ def test_matches_the_oracle(shape, wide, order):
     assert_close(out, d, ids)
 
 
-@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("T", [1, 40, 300, 2100])
 @pytest.mark.parametrize("wide", [False, True])
 def test_ranks_of_their_own(T, wide):
     """Unused rows and columns may hold anything, NaN included; a rank beyond R
@@ -85,7 +86,7 @@ def test_ranks_of_their_own(T, wide):
     assert_close(out, d, ids, ranks)
 
 
-@pytest.mark.parametrize("T", [3, 150])
+@pytest.mark.parametrize("T", [3, 150, 2090])
 @pytest.mark.parametrize("wide", [False, True])
 def test_in_place_strides_and_untouched_rows(T, wide):
     K, N, R, n = 128, 96, 16, 4
@@ -108,10 +109,11 @@ def test_in_place_strides_and_untouched_rows(T, wide):
         assert torch.equal(out, want) and torch.all(big[T:] == 7.0) and torch.all(big[:, 8 + K + N:] == 7.0)
 
 
-def test_special_values_stay_with_their_token():
+@pytest.mark.parametrize("T", [20, 70, 2070])
+def test_special_values_stay_with_their_token(T):
     """A token's NaN or infinity reaches its own row only; tokens without an
     adapter keep every bit."""
-    T, K, N, R, n = 70, 64, 64, 8, 3
+    K, N, R, n = 64, 64, 8, 3
     d = make(T, K, N, R, n, seed=11)
     ids = (torch.arange(T, device=DEV) % 4 - 1).to(torch.int32)
     clean = moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"])
@@ -122,6 +124,23 @@ def test_special_values_stay_with_their_token():
     keep = torch.ones(T, dtype=torch.bool, device=DEV)
     keep[5] = keep[6] = False
     assert torch.equal(out[keep], clean[keep]) and torch.isnan(out[5].float()).all() and not torch.isfinite(out[6].float()).any()
+
+
+@pytest.mark.parametrize("T", [30, 100, 2080])
+def test_special_weights_stay_with_their_adapter(T):
+    """An adapter whose weights are not finite spoils its own tokens only."""
+    K, N, R, n = 96, 64, 16, 4
+    d = make(T, K, N, R, n, seed=12)
+    ids = (torch.arange(T, device=DEV) * 3 % 5 - 1).to(torch.int32)
+    clean = moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"])
+    d["a"][1, 2, 5] = float("inf")
+    d["b"][2, 7, 3] = float("nan")
+    d["scales"][3] = float("nan")
+    out = moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"])
+    for i in (-1, 0):
+        assert torch.equal(out[ids == i], clean[ids == i])
+    bad = ~torch.isfinite(out.float())
+    assert bad[ids == 1].any() and bad[ids == 2][:, 7].all() and not bad[ids == 2][:, :7].any() and bad[ids == 3].all()
 
 
 def test_repeats_bit_for_bit_on_streams_and_graphs():
