@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -155,50 +156,50 @@ def _refuse(msg):
     raise MoeError(MOE_ERR_INVALID_ARG, msg)
 
 
-def _cuda(name, t, dtype, shape, dev=None):
-    """A contiguous CUDA tensor of this dtype and shape, on device dev."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or tuple(t.shape) != shape or \
-            not t.is_contiguous() or (dev is not None and t.device != dev):
-        _refuse(f"{name}: need a contiguous {dtype} CUDA tensor {list(shape)}" + (f" on {dev}" if dev is not None else ""))
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+def _cuda(name, t, dtype, shape, dev):
+    """The address of a contiguous tensor of this dtype and shape on device
+    number dev (None: any CUDA device)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or \
+            (not t.is_cuda if dev is None else t.get_device() != dev):
+        _refuse(f"{name}: need a contiguous {dtype} tensor {list(shape)} on " + ("a CUDA device" if dev is None else f"cuda:{dev}"))
     return t.data_ptr()
 
 
-def _rows(name, t, dtypes, shape, dev):
-    """(address, elements between rows) of a 2-D CUDA tensor whose rows are
-    contiguous; shape entries may be None."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or \
-            (dev is not None and t.device != dev):
-        _refuse(f"{name}: need a 2-D CUDA tensor of {', '.join(str(d) for d in dtypes)}" +
-                (f" on {dev}" if dev is not None else ""))
-    T, W = t.shape
-    if (shape[0] is not None and T != shape[0]) or (shape[1] is not None and W != shape[1]):
-        _refuse(f"{name}: shape {list(t.shape)}, need {list(shape)}")
+def _rows(name, t, dtypes, T, W, dev):
+    """(address, elements between rows) of a tensor [T, W] on device number dev
+    whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.get_device() != dev or t.shape != (T, W):
+        _refuse(f"{name}: need {' or '.join(str(d) for d in dtypes)} [{T}, {W}] on cuda:{dev}")
     s0, s1 = t.stride()
     if s1 != 1 and W > 1:
         _refuse(f"{name}: the elements of a row must be contiguous")
     return t.data_ptr(), s0 if T > 1 else W
 
 
-_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
-_BF16_F32 = (torch.bfloat16, torch.float32)
-
-
-def _on(dev, stream):
-    """(guard, raw stream) of a call on dev's tensors: the guard makes dev
-    current where it is not (null when it is)."""
-    guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    return guard, stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+def _lead(name, t, dtypes):
+    """(T, W, device number) of the 2-D CUDA tensor that sets a call's sizes."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda:
+        _refuse(f"{name}: need a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    T, W = t.shape
+    return T, W, t.get_device()
 
 
 def _call(fn, dev, stream, *args):
-    guard, raw = _on(dev, stream)
-    if guard is None:
-        status = fn(*args, raw)
+    """fn(*args, stream) with device number dev current, on its current stream
+    when none is given."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, stream)
     else:
-        with guard:
-            status = fn(*args, raw)
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
     if status != MOE_OK:
         _check(status)
 
@@ -223,18 +224,18 @@ class Routing:
         if bias is not None and bias.dim() != 1:
             _refuse("Routing: bias must be [E]")
         self.bias = bias
+        self.E = None if bias is None else bias.shape[0]
         self.c = RoutingRule(SCORE[score], num_groups, top_groups, GROUP_SCORE[group_score], int(bool(renorm)), scale,
-                             _cuda("bias", bias, torch.float32, tuple(bias.shape)) if bias is not None else None)
+                             _cuda("bias", bias, torch.float32, (self.E,), None) if bias is not None else None)
 
 
 def select_experts(logits, k, rule, ids=None, w=None, stream=None):
     """fp32 logits [T, E] -> (ids int32 [T, k], weights fp32 [T, k]) under a
     Routing rule (moe_select_experts)."""
-    ptr, ld = _rows("logits", logits, _F32, (None, None), None)
-    T, E = logits.shape
-    dev = logits.device
-    if rule.bias is not None and (rule.bias.shape[0] != E or rule.bias.device != dev):
-        _refuse(f"bias: need {E} entries on {dev}")
+    T, E, dev = _lead("logits", logits, _F32)
+    ptr, ld = _rows("logits", logits, _F32, T, E, dev)
+    if rule.bias is not None and (rule.E != E or rule.bias.get_device() != dev):
+        _refuse(f"bias: need {E} entries on cuda:{dev}")
     if ids is None:
         ids = _new((T, k), torch.int32, dev, stream)
     if w is None:
@@ -259,17 +260,17 @@ def add_adapters(x, y, adapter_ids, a, b, scales, ranks=None, out=None, stream=N
     (moe_add_adapters): x bf16 [T, K], y bf16 or fp32 [T, N], a bf16
     [n, R, K], b bf16 [n, N, R], scales fp32 [n], ranks int32 [n] or None.
     out may be y; by default it is a new tensor."""
-    xp, ldx = _rows("x", x, _BF16, (None, None), None)
-    T, K = x.shape
-    dev = x.device
+    T, K, dev = _lead("x", x, _BF16)
     c = _adapter_set(a, b, scales, ranks, dev)
+    N = c.N
     if c.K != K:
         _refuse(f"a: {c.K} columns, x has {K}")
-    yp, ldy = _rows("y", y, _BF16_F32, (T, c.N), dev)
+    xp, ldx = _rows("x", x, _BF16, T, K, dev)
+    yp, ldy = _rows("y", y, _BF16_F32, T, N, dev)
     if out is None:
-        out = _new((T, c.N), y.dtype, dev, stream)
-    op, ldo = _rows("out", out, (y.dtype,), (T, c.N), dev)
-    _call(lib().moe_add_adapters, dev, stream, xp, ldx, yp, ldy, op, ldo, int(y.dtype is torch.float32), T,
+        out = _new((T, N), y.dtype, dev, stream)
+    op, ldo = (yp, ldy) if out is y else _rows("out", out, (y.dtype,), T, N, dev)
+    _call(lib().moe_add_adapters, dev, stream, xp, ldx, yp, ldy, op, ldo, y.dtype is torch.float32, T,
           _cuda("adapter_ids", adapter_ids, torch.int32, (T,), dev), c)
     return out
 
@@ -277,12 +278,15 @@ def add_adapters(x, y, adapter_ids, a, b, scales, ranks=None, out=None, stream=N
 def _gate(gate, T, H, dev):
     """(kind, address, elements between rows) of a gate tensor by its shape."""
     if gate is None:
-        return GATE["none"], None, 0
+        return 0, 0, 0
     if gate.dim() == 2:
-        return (GATE["element"],) + _rows("gate", gate, _BF16, (T, H), dev)
+        return (GATE["element"],) + _rows("gate", gate, _BF16, T, H, dev)
     if gate.dtype is torch.float32:
         return GATE["token"], _cuda("gate", gate, torch.float32, (T,), dev), 0
     return GATE["channel"], _cuda("gate", gate, torch.bfloat16, (H,), dev), 0
+
+
+_NORM = struct.Struct("@7P5q6i3f4x")
 
 
 def block_norm(r, y=None, post_weight=None, gate=None, gate_sigmoid=False, pre_weight=None, eps=1e-6, branch_scale=1.0,
@@ -291,26 +295,25 @@ def block_norm(r, y=None, post_weight=None, gate=None, gate_sigmoid=False, pre_w
     r bf16 or fp32 [T, H], y bf16 [T, H], weights bf16 [H]; gate bf16 [H]
     (channel), fp32 [T] (token) or bf16 [T, H] (element).  Returns (r', x);
     x is None without pre_weight.  r_out may be r, x_out may be y."""
-    rp, ldr = _rows("r", r, _BF16_F32, (None, None), None)
-    T, H = r.shape
-    dev = r.device
-    n = Norm(r=rp, ld_r=ldr, T=T, H=H, r_fp32=r.dtype is torch.float32, gate_sigmoid=bool(gate_sigmoid),
-             unit_offset=bool(unit_offset), eps=eps, branch_scale=branch_scale, residual_scale=residual_scale)
-    if y is not None:
-        n.y, n.ld_y = _rows("y", y, _BF16, (T, H), dev)
-    if post_weight is not None:
-        n.w_post = _cuda("post_weight", post_weight, torch.bfloat16, (H,), dev)
-    n.gate_kind, n.gate, n.ld_gate = _gate(gate, T, H, dev)
+    T, H, dev = _lead("r", r, _BF16_F32)
+    rp, ldr = _rows("r", r, _BF16_F32, T, H, dev)
+    yp, ldy = _rows("y", y, _BF16, T, H, dev) if y is not None else (0, 0)
+    wpost = _cuda("post_weight", post_weight, torch.bfloat16, (H,), dev) if post_weight is not None else 0
+    kind, gp, ldg = _gate(gate, T, H, dev)
     if r_out is None:
         r_out = _new((T, H), r.dtype, dev, stream)
-    n.r_out, n.ld_r_out = _rows("r_out", r_out, (r.dtype,), (T, H), dev)
+    rop, ldro = (rp, ldr) if r_out is r else _rows("r_out", r_out, (r.dtype,), T, H, dev)
+    wpre = xop = ldx = 0
     if pre_weight is not None:
-        n.w_pre = _cuda("pre_weight", pre_weight, torch.bfloat16, (H,), dev)
+        wpre = _cuda("pre_weight", pre_weight, torch.bfloat16, (H,), dev)
         if x_out is None:
             x_out = _new((T, H), torch.bfloat16, dev, stream)
-        n.x_out, n.ld_x = _rows("x_out", x_out, _BF16, (T, H), dev)
+        xop, ldx = _rows("x_out", x_out, _BF16, T, H, dev)
     elif x_out is not None:
         _refuse("x_out: needs pre_weight")
+    n = Norm.from_buffer_copy(_NORM.pack(rp, yp, wpost, gp, wpre, rop, xop, ldr, ldy, ldg, ldro, ldx, T, H,
+                                         r.dtype is torch.float32, kind, bool(gate_sigmoid), bool(unit_offset), eps,
+                                         branch_scale, residual_scale))
     _call(lib().moe_block_norm, dev, stream, n)
     return r_out, x_out
 
@@ -382,7 +385,7 @@ class MoeLayer:
     def set_routing(self, rule, stream=None):
         """Follow a Routing rule in route, route_from_logits, route_forward and
         block_forward (None: softmax and top-k again)."""
-        if rule is not None and rule.bias is not None and rule.bias.shape[0] != self.cfg.num_experts:
+        if rule is not None and rule.bias is not None and rule.E != self.cfg.num_experts:
             _refuse(f"bias: need {self.cfg.num_experts} entries")
         _check(lib().moe_set_routing(self.h, rule.c if rule is not None else None, _stream(stream)), self.h)
         self._rule = rule          # its bias outlives the asynchronous copy
@@ -393,7 +396,7 @@ class MoeLayer:
         """One MoE block (moe_block_forward): x = norm(r, w_in), the layer x -> y
         with its adapters, r and x_next = block_norm(r, y).  Adapters are
         (a, b, scales, ranks or None) tuples; r is updated in place."""
-        dev = torch.device("cuda", self.cfg.device)
+        dev = self.cfg.device
         H, E, k = self.cfg.hidden, self.cfg.num_experts, self.cfg.top_k
         T = r.shape[0]
         if r.dtype not in _BF16_F32:
