@@ -239,11 +239,13 @@ MOE_DEV void rank_fast(int C, SelScratch& sc) {
     const uint4* quads = reinterpret_cast<const uint4*>(sc.key);
     int r0 = 0, r1 = 0;
     if (C <= 32) {
+#pragma unroll 4
         for (int j = 0; j < (C + 3) / 4; ++j) {
             const uint4 x = quads[j];
             r0 += (x.x > k0) + (x.y > k0) + (x.z > k0) + (x.w > k0);
         }
     } else {
+#pragma unroll 4
         for (int j = 0; j < (C + 3) / 4; ++j) {
             const uint4 x = quads[j];
             r0 += (x.x > k0) + (x.y > k0) + (x.z > k0) + (x.w > k0);
@@ -321,10 +323,10 @@ __device__ __noinline__ int group_rank_exact(const SelectArgs& a, const float* r
 //
 // Error bounds.  ks: of a score.  sigmoid: __expf is off by 2 + 1.173 |x| ulp,
 // which the score sees as at most (4 + 0.37 x 2.4) x 2^-24 absolute, plus 3 ulp
-// of the addition and the division: 1e-6 is over twice that.  softmax: expf 2
-// ulp, rounding of x - top at most 0.37 x 2^-24 of the largest score 1/S, the
+// of the addition and the division: 1e-6 is over twice that.  softmax: __expf
+// (as above, and x - top rounded) 5 x 2^-24 of the largest score 1/S, the
 // sum S 32 terms in a row, 5 folds and its terms' own errors (the mean of
-// top - x under the softmax is at most ln 1024): 3.5e-6 / S; 5e-6 / S is taken.
+// top - x under the softmax is at most ln 1024): 4e-6 / S; 5e-6 / S is taken.
 // A key adds half a step, 2^-24 of its size.
 //
 // Threshold: each lane's two largest keys; t is reached by at least k of them,
@@ -354,7 +356,7 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
 #pragma unroll
     for (int i = 0; i < CH; ++i) load4(row, first(i), -FLT_MAX, v + 4 * i);
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) v[i] = fmaxf(v[i], -FLT_MAX);        // NaN and -inf too
+    for (int i = 0; i < SLOTS; ++i) v[i] = fminf(fmaxf(v[i], -FLT_MAX), FLT_MAX);      // NaN and -inf are off, +inf is capped
     const bool top2 = a.G > 1 && a.top2 && a.per > 1;
     const bool scored = a.bias != nullptr || top2;   // keys or group scores need the scores
     float top = -FLT_MAX, total = 1.0f, ks = 1e-6f;
@@ -371,27 +373,36 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
         }
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) top = fmaxf(top, v[i]);
-        top = fminf(warp_max(top), FLT_MAX);
+        top = warp_max(top);
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) s += sel_on(v[i]) ? expf(sel_cap(v[i]) - top) : 0.0f;
+        for (int i = 0; i < SLOTS; ++i) s += __expf(v[i] - top);     // 0 for those that are off
         total = warp_sum(s);
-        ks = __fdividef(5e-6f, total);
+        // without a bias the groups compare exp(l - top) itself, total times the scores
+        ks = a.bias ? __fdividef(5e-6f, total) : 5e-6f;
     }
     if (scored || a.G > 1) {
-        const float inv = __fdividef(1.0f, total);
+        const float inv = a.bias ? __fdividef(1.0f, total) : 1.0f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int e = first(i);
             float b[4] = {0.0f, 0.0f, 0.0f, 0.0f}, g[4];
             if (a.bias) load4(a.bias, e, -FLT_MAX, b);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float& x = v[4 * i + q];
-                float key = sel_cap(x);
-                if (scored) key = a.sigmoid ? rcp_approx(1.0f + __expf(-x)) : expf(key - top) * inv;
-                if (a.bias) key += sel_cap(b[q]);
-                g[q] = sel_on(x) && sel_on(b[q]) ? key : -INFINITY;
-                if (a.bias) x = g[q];
+            for (int q = 0; q < 4; ++q) g[q] = v[4 * i + q];
+            if (scored) {
+                if (a.sigmoid) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) g[q] = rcp_approx(1.0f + __expf(-g[q]));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) g[q] = __expf(g[q] - top) * inv;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) g[q] = sel_on(v[4 * i + q]) && sel_on(b[q]) ? g[q] + sel_cap(b[q]) : -INFINITY;
+            if (a.bias) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[4 * i + q] = g[q];
             }
             if (VEC) {
                 if (e < a.E) *reinterpret_cast<float4*>(gkey + e) = make_float4(g[0], g[1], g[2], g[3]);
@@ -417,17 +428,22 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
             const bool quads = VEC && (a.per & 3) == 0;
             const int m = quads ? a.per >> 2 : a.per, nit = (m + L - 1) >> gl;
             int it = g % nit;
-            for (int n = 0; n < nit; ++n) {
-                const int j = sub + (it << gl);
-                if (j < m) {
-                    if (quads) {
-                        const float4 x = *reinterpret_cast<const float4*>(gkey + g * a.per + 4 * j);
-                        take(x.x); take(x.y); take(x.z); take(x.w);
-                    } else {
-                        take(gkey[g * a.per + j]);
-                    }
+            if (quads) {
+#pragma unroll 4
+                for (int n = 0; n < nit; ++n) {
+                    const int j = sub + (it << gl);
+                    const float4 x = j < m ? *reinterpret_cast<const float4*>(gkey + g * a.per + 4 * j)
+                                           : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    take(x.x); take(x.y); take(x.z); take(x.w);
+                    it = it + 1 == nit ? 0 : it + 1;
                 }
-                it = it + 1 == nit ? 0 : it + 1;
+            } else {
+#pragma unroll 4
+                for (int n = 0; n < nit; ++n) {
+                    const int j = sub + (it << gl);
+                    take(j < m ? gkey[g * a.per + j] : -INFINITY);
+                    it = it + 1 == nit ? 0 : it + 1;
+                }
             }
         }
         __syncwarp();
@@ -439,6 +455,7 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
         const float mine = top2 && b2 > -INFINITY ? b1 + b2 : b1;
         // rank of this lane's group: lane g << gl speaks for group g
         int rank = 0;
+#pragma unroll 4
         for (int q = 0; q < a.G; ++q) {
             const float x = __shfl_sync(all, mine, q << gl);
             rank += (x > mine || (x == mine && q < g)) ? 1 : 0;
@@ -477,7 +494,7 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
         f2 = fmaxf(f2, fminf(f1, v[i]));
         f1 = fmaxf(f1, v[i]);
     }
-    const uint32_t m1 = sel_on(f1) ? sel_key(sel_cap(f1)) : 0u, m2 = sel_on(f2) ? sel_key(sel_cap(f2)) : 0u;
+    const uint32_t m1 = sel_on(f1) ? sel_key(f1) : 0u, m2 = sel_on(f2) ? sel_key(f2) : 0u;
     uint32_t lo = max(__reduce_min_sync(all, m1), 1u), hi = __reduce_max_sync(all, m1);
     if (hi == 0) {                                   // nothing eligible: experts 0 .. k-1, weights 0
         store_weights(a, t, lane, 0.0f, false, 0.0f, 1.0f);
