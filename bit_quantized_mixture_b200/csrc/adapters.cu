@@ -20,6 +20,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kAdTokenMax = 64;      // up to this T a cluster per token
 constexpr int kAdSmallTile = 2048;   // up to this T tiles of 16 tokens, then of 64
+constexpr int kAdTcMin = 2048;       // from this T on tiles of 128 on the tensor cores
 constexpr int kAdThreads = 256;
 constexpr int kAdCluster = 8;
 
@@ -380,6 +381,10 @@ cudaError_t launch_tiles(const AdapterArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st) {
+    if (a.T >= kAdTcMin) {
+        const cudaError_t e = launch_add_adapters_tc(a, st);
+        if (e != cudaErrorNotSupported) return e;
+    }
     if (a.T > kAdTokenMax) return a.T > kAdSmallTile ? launch_tiles<2, 2>(a, st) : launch_tiles<1, 1>(a, st);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.T * kAdCluster);

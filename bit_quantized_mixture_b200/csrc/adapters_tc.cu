@@ -1,0 +1,646 @@
+// Low-rank adapters of many requests for many tokens, on the tensor cores:
+//   out_t = y_t + B_i (scale_i A_i x_t),   i = adapter of token t.
+//
+// A cluster of CTAs takes 128 consecutive tokens; CTA c has its share of the K
+// columns of x for the first product and of the N columns of y for the second.
+//
+//   1. z: tcgen05.mma, M = the 128 tokens, N = the rank, over 64-column chunks of
+//      x and of the tile's adapters' A (TMA, 128-byte swizzle).  As many adapters
+//      as 256 accumulator columns hold share one pass over x; each row keeps its
+//      own adapter's columns (a tile of one adapter, or of two neighbours, needs
+//      one pass).
+//   2. The cluster's partial sums: each CTA owns 128 / CL of the rows; the others
+//      write their sums for these into its shared memory, it adds them (in the
+//      CTAs' order), and writes z times its scale as the bf16 operand of step 3
+//      into every CTA's.  All remote traffic is stores, whose latency nobody
+//      waits for (reading the others' sums took 5 to 8 us of a tile's 30).
+//   3. out: per chunk of 64 (fp32: 32) output columns and adapter of the tile, one
+//      accumulator of Z B_i^T; rows of that adapter add it to their y, which TMA
+//      brought into the same ring that x came through (it fills while the sums
+//      of step 2 meet), and TMA stores the chunk.
+//
+// A row's results come from its own adapter's accumulators alone, so weights that
+// are not finite spoil no other adapter's tokens.  z is held in bf16 (half a step
+// 2^-8 of a term that is then rounded into a bf16 output), for fp32 outputs in two
+// bf16 halves (2^-16).
+//
+// Warps: 0 loads x and y, 11-12 A and B (TMA; one thread for all of it spends longer on
+// its waits and loads than a chunk takes), 1-2 MMA issuers, 3-10 epilogue (two groups
+// of a thread per row), 13 cleans B's unused columns, 14 stores.
+// Bound by memory: x and y in, out once; the adapters come from L2.
+#include <cooperative_groups.h>
+#include <cuda.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace sm100;
+namespace cg = cooperative_groups;
+
+constexpr int kTcRows = 128;
+constexpr int kTcEpiWarps = 8;           // 4 per stream
+constexpr int kTcSmall = 11, kTcCleaner = 13, kTcStore = 14;     // warps
+constexpr int kTcThreads = 32 * (kTcStore + 1);
+// Two of everything per chunk: an MMA issuer waits, issues and commits for about
+// 700 cycles per chunk of x, and the epilogue of an output chunk is a chain of
+// about 1270, where a chunk's way from memory takes 700 and 1400.  So two issuers
+// and two epilogue groups take turns by chunk, each with rings and accumulators of its own (a parity wait
+// tells only a slot's next use from the last: whoever waits has to see every use).
+constexpr int kTcStreams = 2;
+constexpr int kTcTmemCols = 512;
+constexpr int kTcZCols = 256;            // z: adapters of a pass x streams x rank
+constexpr int kTcDBufs = 2;              // output accumulators of a stream (64 columns each)
+constexpr int kTcCtas = 148;             // SMs of the device: what the tile split aims at
+
+// RB: blocks of 64 rank columns; WIDE: y and out fp32
+template <int RB, bool WIDE>
+struct TcCfg {
+    static constexpr int NC = WIDE ? 32 : 64;               // output columns of a chunk: 128 bytes of a row
+    static constexpr int BIG = kTcRows * 128;               // a chunk of x or y
+    static constexpr int SMALL = RB * 64 * 128;             // a chunk of one A, or of one B
+    // slots of each stream's rings
+    static constexpr int NBIG = RB == 1 ? (WIDE ? 2 : 3) : 2, NSMALL = RB == 1 ? 4 : 1;
+    static constexpr int OFF_SMALL = kTcStreams * NBIG * BIG;
+    static constexpr int OFF_Z = OFF_SMALL + kTcStreams * NSMALL * SMALL;        // fp32 sums of the rows that this CTA owns, by source CTA
+    static constexpr int ZBLOCK = kTcRows * 128;                    // 64 columns of the bf16 operand
+    static constexpr int OFF_OP = OFF_Z + RB * 64 * kTcRows * 4;
+    static constexpr size_t BYTES = OFF_OP + RB * (WIDE ? 2 : 1) * ZBLOCK + 1024;   // base rounded up to the swizzle's 1024
+};
+
+struct TcMaps {
+    CUtensorMap x, y, out, a, b;
+};
+
+MOE_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+                 ::"r"(smem_u32(dst)), "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+// arrive on the barrier at the same place in CTA `rank` of the cluster,
+// releasing this thread's earlier writes to the cluster
+MOE_DEV void mbar_arrive_cluster(uint64_t* bar, int rank) {
+    asm volatile("{ .reg .b32 ra; mapa.shared::cluster.u32 ra, %0, %1;\n"
+                 "  mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra]; }"
+                 ::"r"(smem_u32(bar)), "r"(rank) : "memory");
+}
+// 16 bytes to the same place in CTA `rank` of the cluster
+MOE_DEV void st_cluster_v4(void* p, int rank, uint4 v) {
+    asm volatile("{ .reg .b32 ra; mapa.shared::cluster.u32 ra, %0, %1;\n"
+                 "  st.shared::cluster.v4.b32 [ra], {%2, %3, %4, %5}; }"
+                 ::"r"(smem_u32(p)), "r"(rank), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+MOE_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+MOE_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// bounded wait that acquires what the cluster's arrivals released
+MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            if (err) atomicCAS(err, 0, code);
+            return false;
+        }
+    }
+}
+MOE_DEV bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
+}
+// 16-byte piece j of row r of a 128-byte-swizzled tile
+MOE_DEV uint32_t sw_piece(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
+
+// The chunks lo .. hi - 1 in order, started at another one (any integer turn)
+struct Turned {
+    int at, lo, hi;
+    MOE_DEV Turned(int l, int h, int turn) : at(l + turn % max(h - l, 1)), lo(l), hi(h) {}
+    MOE_DEV void next() {
+        if (++at == hi) at = lo;
+    }
+};
+
+// A place in a ring of N slots and the parity of its use
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    MOE_DEV void next() {
+        if (++slot == N) { slot = 0; phase ^= 1u; }
+    }
+};
+// a wait that ends by itself after a while, whatever the barrier does
+MOE_DEV void wait_some(uint64_t* bar, uint32_t parity) {
+    for (int q = 0; q < 1000 && !mbar_try_wait(bar, parity); ++q) {}
+}
+
+template <int RB, bool WIDE>
+__global__ void __launch_bounds__(kTcThreads, 1)
+k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMaps maps, int rows_a, int per_pass) {
+    using C = TcCfg<RB, WIDE>;
+    constexpr int NBIG = C::NBIG, NSMALL = C::NSMALL, NC = C::NC;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t big_full[kTcStreams][NBIG], big_empty[kTcStreams][NBIG], chunk_done[kTcStreams][NBIG];
+    __shared__ uint64_t small_full[kTcStreams][NSMALL], small_empty[kTcStreams][NSMALL], small_clean[kTcStreams][NSMALL];
+    __shared__ uint64_t z_full, z_free, z_ready, op_full;
+    __shared__ uint64_t d_full[kTcStreams][kTcDBufs], d_empty[kTcStreams][kTcDBufs];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ int s_id[kTcRows], s_list[kTcRows], s_rank[kTcRows];
+    __shared__ unsigned s_first[4];
+    __shared__ float s_scale[kTcRows];
+    // the swizzle and its descriptors count from 1024-byte boundaries
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    cg::cluster_group cl = cg::this_cluster();
+    const int CL = (int)cl.num_blocks(), crank = (int)cl.block_rank();
+    const int t0 = (int)(blockIdx.x / CL) * kTcRows;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nk = (a.K + 63) / 64, nn = (a.N + NC - 1) / NC;
+    const int k0 = (int)((long long)nk * crank / CL), k1 = (int)((long long)nk * (crank + 1) / CL);
+    const int n0 = (int)((long long)nn * crank / CL), n1 = (int)((long long)nn * (crank + 1) / CL);
+    const int early = min(3, k1 - k0);       // (more would keep the adapters' ids waiting behind them)
+    // each tile starts its chunks elsewhere, so that not all CTAs ask for the
+    // same lines of A and B at once
+    const int turn = t0 / kTcRows * 5 % 4096;
+
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kTcStreams; ++w) {
+            for (int i = 0; i < NBIG; ++i) { mbar_init(&big_full[w][i], 1); mbar_init(&big_empty[w][i], 1); mbar_init(&chunk_done[w][i], kTcEpiWarps / kTcStreams); }
+            for (int i = 0; i < NSMALL; ++i) {
+                mbar_init(&small_full[w][i], 1);
+                mbar_init(&small_empty[w][i], 1);
+                mbar_init(&small_clean[w][i], 1);
+            }
+            for (int i = 0; i < kTcDBufs; ++i) { mbar_init(&d_full[w][i], 1); mbar_init(&d_empty[w][i], kTcEpiWarps / kTcStreams); }
+        }
+        mbar_init(&z_full, (uint32_t)min(kTcStreams, k1 - k0));
+        mbar_init(&z_free, kTcEpiWarps);
+        mbar_init(&z_ready, (uint32_t)(kTcEpiWarps * CL));
+        mbar_init(&op_full, (uint32_t)(kTcEpiWarps * CL));
+        abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+        // x needs nothing of the adapters: its first chunks are on their way
+        // while their list is made
+        Turned kc(k0, k1, turn);
+        for (int i = 0; i < early; ++i, kc.next()) {
+            const int w = i & (kTcStreams - 1), slot = i / kTcStreams;
+            mbar_arrive_expect_tx(&big_full[w][slot], C::BIG);
+            tma_load_2d(smem + (w * NBIG + slot) * C::BIG, &maps.x, 64 * kc.at, t0, &big_full[w][slot]);
+        }
+    }
+    if (warp == 1) tmem_alloc(&tmem_slot, kTcTmemCols);
+    if (warp == kTcCleaner && lane < 3) {
+        const CUtensorMap* p = lane == 0 ? &maps.a : (lane == 1 ? &maps.b : &maps.y);
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)p) : "memory");
+    }
+
+    // the tile's adapters in order of their first row, and each row's place among them
+    auto rank_of = [&](int id) { return min(a.ranks ? __ldg(a.ranks + id) : a.R, a.R); };
+    int my_id = -1;
+    if (threadIdx.x < kTcRows) {
+        const int t = t0 + (int)threadIdx.x;
+        const int id = t < a.T ? __ldg(a.ids + t) : -1;
+        if (id >= 0 && id < a.n && rank_of(id) > 0) my_id = id;
+        s_id[threadIdx.x] = my_id;
+    }
+    __syncthreads();
+    cluster_arrive();                        // this CTA's barriers are there for remote arrivals (waited for before the first)
+    bool leads = false;                      // the first row of its adapter
+    if (threadIdx.x < kTcRows) {
+        const unsigned same = __match_any_sync(0xffffffffu, my_id);
+        leads = my_id >= 0 && lane == __ffs(same) - 1;
+        for (unsigned todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
+            const int l = __ffs(todo) - 1, id = __shfl_sync(0xffffffffu, my_id, l);
+            bool seen = false;               // in an earlier warp's rows
+            for (int w = 0; w < warp; ++w) seen = seen || s_id[32 * w + lane] == id;
+            if (__any_sync(0xffffffffu, seen) && lane == l) leads = false;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, leads);
+        if (lane == 0) s_first[warp] = m;
+    }
+    __syncthreads();
+    int D = 0;
+    {
+        int before = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w == warp) before = D;
+            D += __popc(s_first[w]);
+        }
+        if (leads) {
+            const int at = before + __popc(s_first[warp] & ((1u << lane) - 1u));
+            s_list[at] = my_id;
+            s_rank[at] = rank_of(my_id);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    const int passes = max(1, (D + per_pass - 1) / per_pass);      // without an adapter x is let through all the same
+
+    // stream w's chunks: lo + w, lo + w + 2, ...
+    auto count = [](int lo, int hi, int w) { return (hi - lo - w + kTcStreams - 1) / kTcStreams; };
+
+    if (warp == 0) {
+        // ------------------------------ producer of x and y (one thread)
+        if (lane == 0) {
+            Ring<NBIG> ring[kTcStreams];
+            bool ok = true;
+            auto send = [&](int i, const CUtensorMap* map, int col, bool out) {
+                Ring<NBIG>& r = ring[i & (kTcStreams - 1)];
+                const int w = i & (kTcStreams - 1);
+                if (!out) {
+                    ok = mbar_wait(&big_empty[w][r.slot], r.phase ^ 1u, &abort_flag, a.err, 41);
+                    if (!ok) return;
+                    mbar_arrive_expect_tx(&big_full[w][r.slot], C::BIG);
+                    tma_load_2d(smem + (w * NBIG + r.slot) * C::BIG, map, col, t0, &big_full[w][r.slot]);
+                }
+                r.next();
+            };
+            for (int p = 0; ok && p < passes; ++p) {
+                Turned kc(k0, k1, turn);
+                // the first ones went out at the start, into slots not used before
+                for (int i = 0; ok && i < k1 - k0; ++i, kc.next()) send(i, &maps.x, 64 * kc.at, p == 0 && i < early);
+            }
+            Turned nc(n0, n1, turn);
+            for (int i = 0; ok && i < n1 - n0; ++i, nc.next()) send(i, &maps.y, NC * nc.at, false);
+            if (!ok)                                 // given up: let what is in flight land (bounded)
+                for (int w = 0; w < kTcStreams; ++w)
+                    // the slots before the current one in this round of the ring,
+                    // the others in the round before (a slot not used yet in that
+                    // round reads as complete)
+                    for (int i = 0; i < NBIG; ++i) wait_some(&big_full[w][i], i < ring[w].slot ? ring[w].phase : ring[w].phase ^ 1u);
+        }
+        __syncwarp();
+    } else if (warp == kTcSmall || warp == kTcSmall + 1) {
+        // ------------------ producers of A and B, one stream each (one thread)
+        if (lane == 0) {
+            const int w = warp - kTcSmall;
+            Ring<NSMALL> r;
+            bool ok = true;
+            uint8_t* slots = smem + C::OFF_SMALL + w * NSMALL * C::SMALL;
+            for (int p = 0; ok && p < passes; ++p) {
+                const int d0 = p * per_pass, d1 = min(D, d0 + per_pass);
+                Turned kc(k0, k1, turn);
+                for (int i = 0; ok && i < k1 - k0; ++i, kc.next()) {
+                    if ((i & (kTcStreams - 1)) != w) continue;
+                    for (int d = d0; d < d1; ++d, r.next()) {
+                        if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, a.err, 42))) break;
+                        mbar_arrive_expect_tx(&small_full[w][r.slot], (uint32_t)rows_a * 128u);
+                        tma_load_3d(slots + r.slot * C::SMALL, &maps.a, 64 * kc.at, 0, s_list[d], &small_full[w][r.slot]);
+                    }
+                }
+            }
+            Turned nc(n0, n1, turn);
+            for (int i = 0; ok && i < n1 - n0; ++i, nc.next()) {
+                if ((i & (kTcStreams - 1)) != w) continue;
+                for (int d = 0; d < D; ++d, r.next()) {
+                    if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, a.err, 44))) break;
+                    const int nb = (s_rank[d] + 63) / 64;
+                    mbar_arrive_expect_tx(&small_full[w][r.slot], (uint32_t)(nb * NC * 128));
+                    for (int b = 0; b < nb; ++b)
+                        tma_load_3d(slots + r.slot * C::SMALL + b * NC * 128, &maps.b, 64 * b, NC * nc.at, s_list[d], &small_full[w][r.slot]);
+                }
+            }
+            if (!ok)
+                for (int i = 0; i < NSMALL; ++i) wait_some(&small_full[w][i], i < r.slot ? r.phase : r.phase ^ 1u);
+        }
+        __syncwarp();
+    } else if (warp <= kTcStreams) {
+        // --------------------------------------- MMA issuers (one thread)
+        if (lane == 0) {
+            const int w = warp - 1;
+            Ring<NBIG> big;
+            Ring<NSMALL> small;
+            int unit = 0;                            // this stream's B tiles so far
+            bool ok = true;
+            const uint32_t base = smem_u32(smem);
+            // descriptors of the rings' starts; an address counts in 16 bytes
+            const uint64_t dx = desc_kmajor_sw128(base + w * NBIG * C::BIG), ds = desc_kmajor_sw128(base + C::OFF_SMALL + w * NSMALL * C::SMALL);
+            const uint64_t dz = desc_kmajor_sw128(base + C::OFF_OP);
+            const uint32_t idz = idesc_bf16_f32(kTcRows, rows_a), ido = idesc_bf16_f32(kTcRows, NC);
+            for (int p = 0; ok && p < passes; ++p) {
+                const int nd = min(D - p * per_pass, per_pass);
+                if (p > 0 && !(ok = mbar_wait(&z_free, (uint32_t)(p - 1) & 1u, &abort_flag, a.err, 45))) break;
+                tc_fence_after();
+                for (int kc = k0 + w; ok && kc < k1; kc += kTcStreams, big.next()) {
+                    if (!(ok = mbar_wait(&big_full[w][big.slot], big.phase, &abort_flag, a.err, 46))) break;
+                    const uint64_t xd = dx + (uint64_t)(big.slot * (C::BIG >> 4));
+                    for (int d = 0; d < nd; ++d, small.next()) {
+                        if (!(ok = mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, a.err, 47))) break;
+                        const uint64_t ad = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
+                        const uint32_t dst = tmem + (uint32_t)((d * kTcStreams + w) * rows_a);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mma_bf16(dst, xd + 2 * q, ad + 2 * q, idz, kc > k0 + w || q > 0 ? 1u : 0u);
+                        mma_commit(&small_empty[w][small.slot]);
+                    }
+                    if (ok) mma_commit(&big_empty[w][big.slot]);
+                }
+                if (ok && w < k1 - k0) mma_commit(&z_full);
+            }
+            if (ok && D > 0) {
+                ok = mbar_wait_cluster(&op_full, 0u, &abort_flag, a.err, 48);
+                fence_proxy_async_smem();            // the operand came by ordinary stores
+            }
+            for (int nc = n0 + w; ok && nc < n1; nc += kTcStreams)
+                for (int d = 0; d < D; ++d, small.next(), ++unit) {
+                    const int buf = unit & 1, steps = (s_rank[d] + 15) / 16;
+                    ok = a.ranks ? mbar_wait(&small_clean[w][small.slot], (uint32_t)(unit / NSMALL) & 1u, &abort_flag, a.err, 49)
+                                 : mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, a.err, 49);
+                    ok = ok && mbar_wait(&d_empty[w][buf], ((uint32_t)(unit >> 1) & 1u) ^ 1u, &abort_flag, a.err, 50);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t bd = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
+                    const uint32_t dst = tmem + kTcZCols + 64u * (uint32_t)(w * kTcDBufs + buf);
+                    for (int h = 0; h < (WIDE ? 2 : 1); ++h)
+                        for (int q = 0; q < steps; ++q)
+                            mma_bf16(dst, dz + (uint64_t)((h * RB + (q >> 2)) * (C::ZBLOCK >> 4) + 2 * (q & 3)),
+                                     bd + (uint64_t)((q >> 2) * (NC * 128 >> 4) + 2 * (q & 3)), ido, h + q > 0 ? 1u : 0u);
+                    mma_commit(&small_empty[w][small.slot]);
+                    mma_commit(&d_full[w][buf]);
+                }
+        }
+        __syncwarp();
+    } else if (warp == kTcStore) {
+        // -------------------------------------------- stores (one thread)
+        if (lane == 0) {
+            Ring<NBIG> ring[kTcStreams];                         // phase: of the slot's chunk_done
+            for (int w = 0; w < kTcStreams; ++w) ring[w].slot = passes * count(k0, k1, w) % NBIG;
+            int first[kTcStreams] = {ring[0].slot, ring[1].slot};
+            Turned at(n0, n1, turn);
+            bool ok = true;
+            for (int i = 0; ok && i < n1 - n0; ++i, at.next()) {
+                const int w = i & (kTcStreams - 1), s = ring[w].slot;
+                if (!(ok = mbar_wait(&chunk_done[w][s], ring[w].phase, &abort_flag, a.err, 59))) break;
+                tma_store_2d(&maps.out, NC * at.at, t0, smem + (w * NBIG + s) * C::BIG);
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&big_empty[w][s]);
+                // the ring's round, counted from where the stream's chunks began
+                ring[w].slot = s + 1 == NBIG ? 0 : s + 1;
+                if (ring[w].slot == first[w]) ring[w].phase ^= 1u;
+            }
+            bulk_wait_all();
+        }
+        __syncwarp();
+    } else if (warp == kTcCleaner) {
+        // With ranks of their own, adapters' B columns behind the rank may hold
+        // anything: those of the last k step are zeroed where they arrived.
+        if (a.ranks) {
+            // the first product's uses of the slots are over then, and the slots
+            // go on where it left off
+            bool ok = D == 0 || __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, a.err, 57));
+            int used[kTcStreams];
+            for (int w = 0; w < kTcStreams; ++w) used[w] = D * count(k0, k1, w);
+            for (int nc = n0; ok && nc < n1; ++nc) {
+                const int w = (nc - n0) & (kTcStreams - 1);
+                for (int d = 0; d < D; ++d, ++used[w]) {
+                    const int slot = used[w] % NSMALL;
+                    if (!(ok = all_wait(&small_full[w][slot], (uint32_t)(used[w] / NSMALL) & 1u, &abort_flag, a.err, 56))) break;
+                    const int rank = s_rank[d], steps = (rank + 15) / 16;
+                    if (rank & 15) {
+                        uint8_t* bt = smem + C::OFF_SMALL + (w * NSMALL + slot) * C::SMALL;
+                        for (int i = lane; i < NC * 16; i += 32) {
+                            const int r = i >> 4, col = 16 * (steps - 1) + (i & 15);
+                            if (col >= rank)
+                                *reinterpret_cast<uint16_t*>(bt + (col >> 6) * NC * 128 + sw_piece(r, (col & 63) >> 3) + 2 * (col & 7)) = 0;
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&small_clean[w][slot]);
+                }
+            }
+        }
+    } else {
+        // --------------------------------------------------------- epilogue
+        const int quarter = warp & 3, group = (warp - 3) >> 2, row = quarter * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const int id = s_id[row];
+        int mine = -1;
+        for (int d = 0; id >= 0 && mine < 0; ++d) mine = s_list[d] == id ? d : -1;
+        if (group == 0) s_scale[row] = id >= 0 ? __ldg(a.scales + id) : 0.0f;     // read behind z_ready
+        bool ok = true;
+        cluster_wait();
+        if (D > 0) {
+            // [source CTA][rank / 4][own row]
+            const int own_rows = kTcRows / CL, owner = row / own_rows, quads = rows_a / 4;
+            float4* zp = reinterpret_cast<float4*>(smem + C::OFF_Z);
+            for (int p = 0; ok && p < passes; ++p) {
+                if (!(ok = all_wait(&z_full, (uint32_t)p & 1u, &abort_flag, a.err, 51))) break;
+                tc_fence_after();
+                const int nd = min(D - p * per_pass, per_pass);
+                for (int d = 0; d < nd; ++d) {
+                    const bool own = mine == p * per_pass + d;
+                    if (!__any_sync(0xffffffffu, own)) continue;
+                    for (int c = 16 * group; c < rows_a; c += 32) {
+                        float v[16];
+                        const uint32_t src = tmem + lane_base + (uint32_t)(d * kTcStreams * rows_a + c);
+                        tmem_ld16(src, v);
+                        if (k1 - k0 > 1) {               // the second issuer's chunks
+                            float u[16];
+                            tmem_ld16(src + (uint32_t)rows_a, u);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] += u[e];
+                        }
+                        if (own) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                st_cluster_v4(zp + (crank * quads + c / 4 + q) * own_rows + row % own_rows, owner,
+                                              make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                                                         __float_as_uint(v[4 * q + 3])));
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&z_free);
+            }
+            __syncwarp();
+            if (ok) {
+                if (lane < CL) mbar_arrive_cluster(&z_ready, lane);
+                ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_ready, 0u, &abort_flag, a.err, 52));
+            }
+            if (ok) {
+                uint8_t* op = smem + C::OFF_OP;
+                for (int i = (int)threadIdx.x - 96; i < own_rows * (rows_a / 8); i += kTcEpiWarps * 32) {
+                    const int rl = i % own_rows, j = i / own_rows, r = crank * own_rows + rl;     // row, eight columns
+                    float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    const int rid = s_id[r];
+                    if (rid >= 0) {
+                        const int rank = rank_of(rid);
+                        const float scale = s_scale[r];
+                        for (int q = 0; q < CL; ++q) {
+                            const float4 v0 = zp[(q * quads + 2 * j) * own_rows + rl], v1 = zp[(q * quads + 2 * j + 1) * own_rows + rl];
+                            z[0] += v0.x; z[1] += v0.y; z[2] += v0.z; z[3] += v0.w;
+                            z[4] += v1.x; z[5] += v1.y; z[6] += v1.z; z[7] += v1.w;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) z[q] = 8 * j + q < rank ? z[q] * scale : 0.0f;
+                    }
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        hi[q] = pack_bf16x2(z[2 * q], z[2 * q + 1]);
+                        lo[q] = pack_bf16x2(z[2 * q] - bf16_lo(hi[q]), z[2 * q + 1] - bf16_hi(hi[q]));
+                    }
+                    uint8_t* d = op + (j >> 3) * C::ZBLOCK + sw_piece(r, j & 7);
+                    for (int q = 0; q < CL; ++q) {
+                        st_cluster_v4(d, q, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                        if (WIDE) st_cluster_v4(d + RB * C::ZBLOCK, q, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    }
+                }
+                asm volatile("fence.proxy.async;" ::: "memory");
+                __syncwarp();
+                if (lane < CL) mbar_arrive_cluster(&op_full, lane);
+            }
+        }
+        // The first product's uses of the slots are over (a parity tells only one
+        // use from the next), and this group's chunks, every other one, go on
+        // where its stream left off.
+        if (D == 0) ok = all_wait(&z_full, 0u, &abort_flag, a.err, 58);
+        int unit = 0, big = passes * count(k0, k1, group);
+        for (int nc = n0 + group; ok && nc < n1; nc += kTcStreams, ++big) {
+            const int s = big % NBIG;
+            if (!(ok = all_wait(&big_full[group][s], (uint32_t)(big / NBIG) & 1u, &abort_flag, a.err, 54))) break;
+            uint8_t* tile = smem + (group * NBIG + s) * C::BIG;
+            for (int d = 0; d < D; ++d, ++unit) {
+                const int buf = unit & 1;
+                if (!(ok = all_wait(&d_full[group][buf], (uint32_t)(unit >> 1) & 1u, &abort_flag, a.err, 55))) break;
+                tc_fence_after();
+                if (__any_sync(0xffffffffu, mine == d)) {
+                    const uint32_t src = tmem + lane_base + kTcZCols + 64u * (uint32_t)(group * kTcDBufs + buf);
+                    // 32 output columns at a time: 64 (fp32: 128) bytes of the row
+#pragma unroll
+                    for (int c = 0; c < NC; c += 32) {
+                        uint32_t r[32];
+                        tmem_ld_x32c(src + (uint32_t)c, r);
+                        if (mine == d) {
+#pragma unroll
+                            for (int j = 0; j < (WIDE ? 8 : 4); ++j) {
+                                uint4* p = reinterpret_cast<uint4*>(tile + sw_piece(row, c / 8 + j));
+                                uint4 v = *p;
+                                uint32_t* w = &v.x;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    if (WIDE) w[q] = __float_as_uint(__uint_as_float(w[q]) + __uint_as_float(r[4 * j + q]));
+                                    else w[q] = pack_bf16x2(bf16_lo(w[q]) + __uint_as_float(r[(8 * j + 2 * q) & 31]),
+                                                            bf16_hi(w[q]) + __uint_as_float(r[(8 * j + 2 * q + 1) & 31]));
+                                }
+                                *p = v;
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&d_empty[group][buf]);
+            }
+            if (!ok) break;
+            fence_proxy_async_smem();        // the chunk is stored from where it lies
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&chunk_done[group][s]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kTcTmemCols);
+    if (warp <= kTcStreams || warp >= kTcSmall) cluster_wait();     // of the first arrival
+    cluster_arrive();                        // nobody leaves while others may write to its shared memory
+    cluster_wait();
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// rows of `cols` elements, `ld` elements apart; boxes of 128 bytes x box_rows
+bool map_rows(CUtensorMap* m, const void* base, bool fp32, int rows, int cols, long long ld, int box_rows) {
+    const int es = fp32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * es};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return encode_fn()(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+                       one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// contiguous bf16 [n][rows][cols]; boxes of 64 columns x box_rows of one matrix, zeros past its edges
+bool map_stack(CUtensorMap* m, const void* base, int n, int rows, int cols, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)rows * cols * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int RB, bool WIDE>
+cudaError_t launch_tc(const AdapterArgs& a, cudaStream_t st) {
+    using C = TcCfg<RB, WIDE>;
+    if (!encode_fn()) return cudaErrorNotSupported;
+    const int rows_a = (a.R + 15) / 16 * 16;
+    TcMaps m;
+    if (!map_rows(&m.x, a.x, false, a.T, a.K, a.ld_x, kTcRows) || !map_rows(&m.y, a.y, WIDE, a.T, a.N, a.ld_y, kTcRows) ||
+        !map_rows(&m.out, a.out, WIDE, a.T, a.N, a.ld_out, kTcRows) || !map_stack(&m.a, a.a, a.n, a.R, a.K, rows_a) ||
+        !map_stack(&m.b, a.b, a.n, a.N, a.R, C::NC))
+        return cudaErrorNotSupported;
+    // CTAs for about one wave; no share of K or N is empty
+    const int tiles = (a.T + kTcRows - 1) / kTcRows;
+    const int nk = (a.K + 63) / 64, nn = (a.N + C::NC - 1) / C::NC;
+    auto k = k_adapter_tc<RB, WIDE>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = C::BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    // The largest cluster with which all tiles run at once: its CTAs share a GPC,
+    // so fewer of the larger ones fit (here 74 of 2, 33 of 4, 15 of 8).
+    int cluster = 8;
+    for (; cluster > 1; cluster /= 2) {
+        if (cluster > nk || cluster > nn || tiles * cluster > kTcCtas) continue;
+        at[0].val.clusterDim.x = (unsigned)cluster;
+        cfg.gridDim = dim3((unsigned)(tiles * cluster));
+        int fit = 0;
+        e = cudaOccupancyMaxActiveClusters(&fit, k, &cfg);
+        if (e != cudaSuccess) return e;
+        if (tiles <= fit) break;
+    }
+    at[0].val.clusterDim.x = (unsigned)cluster;
+    cfg.gridDim = dim3((unsigned)(tiles * cluster));
+    return cudaLaunchKernelEx(&cfg, k, a, m, rows_a, kTcZCols / (kTcStreams * rows_a));
+}
+
+}  // namespace
+
+cudaError_t launch_add_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
+    if (a.R <= 64) return a.wide ? launch_tc<1, true>(a, st) : launch_tc<1, false>(a, st);
+    // ranks above 64 with fp32 outputs: sums, operand halves and rings do not fit
+    return a.wide ? cudaErrorNotSupported : launch_tc<2, false>(a, st);
+}
+
+}  // namespace moe

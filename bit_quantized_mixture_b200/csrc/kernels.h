@@ -82,7 +82,11 @@ struct AdapterArgs {
     long long ld_x, ld_y, ld_out;
     int T, K, N, R, n;
     bool wide;              // y and out are fp32
+    int* err;               // device error word (bounded waits) or null
 };
+// adapters_tc.cu: tiles of 128 tokens on the tensor cores (cudaErrorNotSupported:
+// a tensor that no tensor map describes)
+cudaError_t launch_add_adapters_tc(const AdapterArgs& a, cudaStream_t st);
 cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st);
 
 // block_norm.cu

@@ -988,8 +988,9 @@ static moe_status check_adapters(moe_layer* h, const char* fn, const moe_adapter
 }
 
 static AdapterArgs adapter_args(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,
-                                int32_t wide, int32_t T, const int32_t* ids, const moe_adapters* ad) {
+                                int32_t wide, int32_t T, const int32_t* ids, const moe_adapters* ad, int* err = nullptr) {
     AdapterArgs a{};
+    a.err = err;
     a.x = x; a.y = y; a.out = out; a.ids = ids;
     a.a = ad->a; a.b = ad->b; a.scales = ad->scales; a.ranks = ad->ranks;
     a.ld_x = ld_x; a.ld_y = ld_y; a.ld_out = ld_out;
@@ -1132,7 +1133,7 @@ moe_status moe_block_forward(moe_handle h, const moe_block* b, moe_stream_t stre
         float* logits = b->logits ? b->logits : h->logits;
         s = moe_route(h, b->x, T, nullptr, nullptr, logits, stream);
         if (s != MOE_OK) return s;
-        e = launch_add_adapters(adapter_args(b->x, H, logits, E, logits, E, 1, T, b->adapter_ids, b->router_adapters), st);
+        e = launch_add_adapters(adapter_args(b->x, H, logits, E, logits, E, 1, T, b->adapter_ids, b->router_adapters, h->dev_err), st);
         if (e != cudaSuccess) return cuda_fail(h, e, fn);
         s = moe_route_from_logits(h, logits, T, b->topk_ids, b->topk_w, stream);
         if (s == MOE_OK) s = moe_forward(h, b->x, T, b->topk_ids, b->topk_w, b->y, stream);
@@ -1144,7 +1145,7 @@ moe_status moe_block_forward(moe_handle h, const moe_block* b, moe_stream_t stre
     }
     if (s != MOE_OK) return s;
     if (b->layer_adapters) {
-        e = launch_add_adapters(adapter_args(b->x, H, b->y, H, b->y, H, 0, T, b->adapter_ids, b->layer_adapters), st);
+        e = launch_add_adapters(adapter_args(b->x, H, b->y, H, b->y, H, 0, T, b->adapter_ids, b->layer_adapters, h->dev_err), st);
         if (e != cudaSuccess) return cuda_fail(h, e, fn);
     }
     if ((e = run_norm(&n, st)) != cudaSuccess) return cuda_fail(h, e, fn);
