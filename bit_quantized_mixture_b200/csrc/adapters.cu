@@ -3,10 +3,10 @@
 // A_i [R, K], B_i [N, R] (bf16, the first rank_i rows / columns in use), x
 // bf16, y and out bf16 or fp32.  Tokens without an adapter keep y_t.
 //
-// One cluster of CTAs per token: CTA c sums A_i x_t over its share of the K
-// columns (a warp per row of A, lanes along K), the shares meet through
-// distributed shared memory, and CTA c then writes its share of the N
-// outputs, a thread per output.
+// Few tokens: a cluster of CTAs per token.  CTA c sums A_i x_t over its share of
+// the K columns (a warp per four rows of A, lanes along K), writes the sums into
+// every CTA's shared memory, and then has its share of the N outputs, R / 8 lanes
+// per output; the rows of B are on their way meanwhile.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -18,11 +18,22 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kAdTokenMax = 64;      // up to this T a cluster per token
-constexpr int kAdSmallTile = 2048;   // up to this T tiles of 16 tokens, then of 64
-constexpr int kAdTcMin = 2048;       // from this T on tiles of 128 on the tensor cores
+// Which kernel takes a call is a matter of its tokens: whose they are is known on
+// the device alone.  A cluster per token reads each token's whole adapter; tiles
+// share it among the tokens of one request, but go through a tile's adapters one
+// after another.  2048 -> 2048, us, tokens of 64 requests mixed / of 12 requests in
+// order: 128 tokens rank 16, by token 6.4 / 6.4, in tiles of 16 28 / 10; 256 tokens
+// 9.4 / 9.4 and 29 / 9.7; 512 tokens 17 / 17 and 32 / 9.2; rank 64, 128 tokens
+// 21 / 21 and 55 / 15; 256 tokens 38 / 38 and 60 / 15.
+constexpr int kAdTokenMax = 256, kAdTokenWork = 8192;        // most tokens, most tokens x R, of a cluster per token
+// CTAs per token: rank 16, 1 token 3.8 us with 8, 4.6 with 4, 6.9 with 2; 64 tokens
+// 5.6 / 5.4 / 7.1; 128 tokens 9.8 / 6.4 / 7.6; 256 tokens 18 / 11.4 / 9.4.
+constexpr int kAdCluster8 = 32, kAdCluster4 = 192;           // up to so many tokens 8, 4 CTAs
+// Tiles of 16 against 64 tokens: 1024 tokens rank 16 8.7 / 12 us, 4096 tokens 29 / 25;
+// tiles of 128 on tcgen05 (adapters_tc.cu) against those: 2048 tokens rank 16 22 / 15,
+// 4096 tokens 24 / 25, 8192 tokens rank 64 40 / 59.
+constexpr int kAdSmallTile = 2048, kAdTcMin = 2800;
 constexpr int kAdThreads = 256;
-constexpr int kAdCluster = 8;
 
 MOE_DEV float dot8(const uint4& p, const uint4& q, float s) {
     const uint32_t a[4] = {p.x, p.y, p.z, p.w}, b[4] = {q.x, q.y, q.z, q.w};
@@ -34,56 +45,129 @@ MOE_DEV float dot8(const uint4& p, const uint4& q, float s) {
     return s;
 }
 
+MOE_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+MOE_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// LL: log2 of the lanes that share an output (8 of B's columns each).
+template <int CL, int LL>
 __global__ void __launch_bounds__(kAdThreads) k_adapter_token(const __grid_constant__ AdapterArgs a) {
-    __shared__ float part[kAdapterMaxRank];      // this CTA's share of z
-    __shared__ float z[kAdapterMaxRank];
+    constexpr int WARPS = kAdThreads / 32, L = 1 << LL, PER = 32 / L, BATCH = 4;
+    __shared__ float part[CL][kAdapterMaxRank];  // every CTA's share of z, written by them
+    __shared__ __align__(16) float z[kAdapterMaxRank];
     cg::cluster_group cl = cg::this_cluster();
     const int c = (int)cl.block_rank();
-    const size_t t = blockIdx.x / kAdCluster;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const size_t t = blockIdx.x / CL;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & (L - 1);
     const int id = __ldg(a.ids + t);
     const bool has = id >= 0 && id < a.n;
-    int rank = has ? (a.ranks ? __ldg(a.ranks + id) : a.R) : 0;
-    rank = min(max(rank, 0), a.R);
+    const int rank = has ? min(max(a.ranks ? __ldg(a.ranks + id) : a.R, 0), a.R) : 0;
+    const float scale = rank ? __ldg(a.scales + id) : 0.0f;
+    // this CTA's outputs, and the first batch of their rows of B: they need no z
+    const int n0 = (int)((long long)a.N * c / CL), n1 = (int)((long long)a.N * (c + 1) / CL);
+    const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(a.b) + (size_t)(has ? id : 0) * a.N * a.R + 8 * sub;
+    const bool cols = 8 * sub < rank;
+    auto output = [&](int i) { return n0 + (i * WARPS + warp) * PER + lane / L; };
+    uint4 q[BATCH];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int j = output(i0 + u);
+            q[u] = cols && j < n1 ? ldg_nc_v4(b + (size_t)j * a.R) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    fetch(0);
     // K in vectors of 8 columns, shares of whole vectors
     const int kv = a.K / 8;
-    const int k0 = (int)((long long)kv * c / kAdCluster), k1 = (int)((long long)kv * (c + 1) / kAdCluster);
+    const int k0 = (int)((long long)kv * c / CL), k1 = (int)((long long)kv * (c + 1) / CL);
     const uint4* x = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.x) + t * a.ld_x);
-    for (int r = warp; r < rank; r += kAdThreads / 32) {
-        const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.a) + ((size_t)id * a.R + r) * a.K);
-        float s = 0.0f;
-        for (int v = k0 + lane; v < k1; v += 32) s = dot8(__ldg(row + v), __ldg(x + v), s);
-        s = warp_sum(s);
-        if (lane == 0) part[r] = s;
-    }
-    cl.sync();
-    const float scale = rank ? __ldg(a.scales + id) : 0.0f;
-    for (int r = threadIdx.x; r < rank; r += kAdThreads) {
-        float s = 0.0f;
+    cluster_arrive();                            // everyone is here: its shared memory may be written
+    bool here = false;
+    for (int r0 = warp; r0 < rank; r0 += 4 * WARPS) {
+        const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.a) + ((size_t)id * a.R + r0) * a.K);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int v = k0 + lane; v < k1; v += 32) {
+            uint4 p[4];
 #pragma unroll
-        for (int q = 0; q < kAdCluster; ++q) s += cl.map_shared_rank(part, q)[r];
-        z[r] = s * scale;
-    }
-    cl.sync();                                   // z is written; nobody reads part any more
-    const int n0 = (int)((long long)a.N * c / kAdCluster), n1 = (int)((long long)a.N * (c + 1) / kAdCluster);
-    for (int j = n0 + (int)threadIdx.x; j < n1; j += kAdThreads) {
-        const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(a.b) + ((size_t)(has ? id : 0) * a.N + j) * a.R;
-        float s = 0.0f;
-        for (int r0 = 0; r0 < rank; r0 += 8) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4*>(b + r0));
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            for (int u = 0; u < 4; ++u) p[u] = r0 + u * WARPS < rank ? ldg_nc_v4(row + (size_t)u * WARPS * kv + v) : make_uint4(0, 0, 0, 0);
+            const uint4 xv = __ldg(x + v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (r0 + i < rank) s = fmaf((i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]), z[r0 + i], s);
+            for (int u = 0; u < 4; ++u) s[u] = dot8(p[u], xv, s[u]);
         }
-        if (a.wide) {
-            const float y = reinterpret_cast<const float*>(a.y)[t * a.ld_y + j];
-            reinterpret_cast<float*>(a.out)[t * a.ld_out + j] = rank ? y + s : y;
-        } else {
-            const __nv_bfloat16 y = reinterpret_cast<const __nv_bfloat16*>(a.y)[t * a.ld_y + j];
-            reinterpret_cast<__nv_bfloat16*>(a.out)[t * a.ld_out + j] = rank ? __float2bfloat16_rn(bf16_to_f(y) + s) : y;
+        if (!here) cluster_wait();
+        here = true;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            s[u] = warp_sum(s[u]);
+            if (lane < CL && r0 + u * WARPS < rank) *cl.map_shared_rank(&part[c][r0 + u * WARPS], lane) = s[u];
         }
     }
+    if (!here) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    for (int r = threadIdx.x; r < kAdapterMaxRank; r += kAdThreads) {
+        float s = 0.0f;
+        if (r < rank) {
+#pragma unroll
+            for (int u = 0; u < CL; ++u) s += part[u][r];
+        }
+        z[r] = r < rank ? s * scale : 0.0f;
+    }
+    __syncthreads();
+    float zv[8];
+    uint32_t keep[4];                            // columns behind the rank may hold anything
+#pragma unroll
+    for (int i = 0; i < 8; ++i) zv[i] = z[8 * sub + i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        keep[i] = (8 * sub + 2 * i < rank ? 0xffffu : 0u) | (8 * sub + 2 * i + 1 < rank ? 0xffff0000u : 0u);
+    for (int i0 = 0; output(i0) - lane / L < n1; i0 += BATCH) {
+        if (i0) fetch(i0);
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const uint32_t w[4] = {q[u].x & keep[0], q[u].y & keep[1], q[u].z & keep[2], q[u].w & keep[3]};
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s = fmaf(bf16_lo(w[i]), zv[2 * i], s);
+                s = fmaf(bf16_hi(w[i]), zv[2 * i + 1], s);
+            }
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            const int j = output(i0 + u);
+            if (sub != 0 || j >= n1) continue;
+            if (a.wide) {
+                const float y = reinterpret_cast<const float*>(a.y)[t * a.ld_y + j];
+                reinterpret_cast<float*>(a.out)[t * a.ld_out + j] = rank ? y + s : y;
+            } else {
+                const __nv_bfloat16 y = reinterpret_cast<const __nv_bfloat16*>(a.y)[t * a.ld_y + j];
+                reinterpret_cast<__nv_bfloat16*>(a.out)[t * a.ld_out + j] = rank ? __float2bfloat16_rn(bf16_to_f(y) + s) : y;
+            }
+        }
+    }
+}
+
+template <int CL, int LL>
+cudaError_t launch_token(const AdapterArgs& a, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)a.T * CL);
+    cfg.blockDim = dim3(kAdThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CL;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_adapter_token<CL, LL>, a);
+}
+
+template <int CL>
+cudaError_t launch_tokens(const AdapterArgs& a, cudaStream_t st) {
+    if (a.R <= 8) return launch_token<CL, 0>(a, st);
+    if (a.R <= 16) return launch_token<CL, 1>(a, st);
+    if (a.R <= 32) return launch_token<CL, 2>(a, st);
+    if (a.R <= 64) return launch_token<CL, 3>(a, st);
+    return launch_token<CL, 4>(a, st);
 }
 
 // D (16 x 8, fp32) += A (16 x 16, bf16) B (16 x 8, bf16)
@@ -381,22 +465,15 @@ cudaError_t launch_tiles(const AdapterArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st) {
+    if (a.T <= kAdTokenMax && (long long)a.T * a.R <= kAdTokenWork) {
+        if (a.T <= kAdCluster8) return launch_tokens<8>(a, st);
+        return a.T <= kAdCluster4 ? launch_tokens<4>(a, st) : launch_tokens<2>(a, st);
+    }
     if (a.T >= kAdTcMin) {
         const cudaError_t e = launch_add_adapters_tc(a, st);
         if (e != cudaErrorNotSupported) return e;
     }
-    if (a.T > kAdTokenMax) return a.T > kAdSmallTile ? launch_tiles<2, 2>(a, st) : launch_tiles<1, 1>(a, st);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)a.T * kAdCluster);
-    cfg.blockDim = dim3(kAdThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kAdCluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_adapter_token, a);
+    return a.T <= kAdSmallTile ? launch_tiles<1, 1>(a, st) : launch_tiles<2, 2>(a, st);
 }
 
 }  // namespace moe

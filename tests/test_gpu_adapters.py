@@ -52,7 +52,9 @@ def assert_close(out, d, ids, ranks=None):
 
 SHAPES = [(1, 2048, 2048, 16, 3), (1, 8, 8, 8, 1), (2, 72, 40, 24, 2), (7, 256, 512, 128, 4), (16, 512, 264, 40, 5), (17, 520, 1000, 8, 3),
           (61, 1024, 512, 32, 40), (130, 264, 136, 64, 6), (200, 2048, 256, 16, 11), (333, 136, 72, 56, 2),
-          (2113, 136, 72, 24, 7), (2305, 64, 96, 64, 30), (2200, 72, 40, 128, 3), (2049, 520, 264, 96, 4)]
+          (2113, 136, 72, 24, 7), (2305, 64, 96, 64, 30), (2200, 72, 40, 128, 3), (2049, 520, 264, 96, 4),
+          (2801, 136, 72, 24, 7), (2817, 64, 96, 64, 30), (2900, 72, 40, 128, 3), (3000, 520, 264, 96, 4), (2800, 1032, 520, 16, 1), (4001, 128, 64, 8, 2),
+          (100, 256, 264, 72, 3), (240, 64, 72, 32, 4), (60, 72, 1000, 128, 2)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -70,7 +72,7 @@ def test_matches_the_oracle(shape, wide, order):
     assert_close(out, d, ids)
 
 
-@pytest.mark.parametrize("T", [1, 40, 300, 2100])
+@pytest.mark.parametrize("T", [1, 40, 200, 300, 2100, 2900])
 @pytest.mark.parametrize("wide", [False, True])
 def test_ranks_of_their_own(T, wide):
     """Unused rows and columns may hold anything, NaN included; a rank beyond R
@@ -86,7 +88,7 @@ def test_ranks_of_their_own(T, wide):
     assert_close(out, d, ids, ranks)
 
 
-@pytest.mark.parametrize("T", [3, 150, 2090])
+@pytest.mark.parametrize("T", [3, 150, 400, 2090, 2830])
 @pytest.mark.parametrize("wide", [False, True])
 def test_in_place_strides_and_untouched_rows(T, wide):
     K, N, R, n = 128, 96, 16, 4
@@ -109,7 +111,7 @@ def test_in_place_strides_and_untouched_rows(T, wide):
         assert torch.equal(out, want) and torch.all(big[T:] == 7.0) and torch.all(big[:, 8 + K + N:] == 7.0)
 
 
-@pytest.mark.parametrize("T", [20, 70, 2070])
+@pytest.mark.parametrize("T", [20, 70, 300, 2070, 2870])
 def test_special_values_stay_with_their_token(T):
     """A token's NaN or infinity reaches its own row only; tokens without an
     adapter keep every bit."""
@@ -126,7 +128,7 @@ def test_special_values_stay_with_their_token(T):
     assert torch.equal(out[keep], clean[keep]) and torch.isnan(out[5].float()).all() and not torch.isfinite(out[6].float()).any()
 
 
-@pytest.mark.parametrize("T", [30, 100, 2080])
+@pytest.mark.parametrize("T", [30, 100, 280, 2080, 2880])
 def test_special_weights_stay_with_their_adapter(T):
     """An adapter whose weights are not finite spoils its own tokens only."""
     K, N, R, n = 96, 64, 16, 4
@@ -143,10 +145,11 @@ def test_special_weights_stay_with_their_adapter(T):
     assert bad[ids == 1].any() and bad[ids == 2][:, 7].all() and not bad[ids == 2][:, :7].any() and bad[ids == 3].all()
 
 
-def test_repeats_bit_for_bit_on_streams_and_graphs():
-    T, K, N, R, n = 150, 512, 512, 16, 5
+@pytest.mark.parametrize("T", [150, 700, 4100])
+def test_repeats_bit_for_bit_on_streams_and_graphs(T):
+    K, N, R, n = 512, 512, 16, 5
     d = make(T, K, N, R, n, seed=2)
-    ids = (torch.arange(T, device=DEV) // 40).to(torch.int32)
+    ids = (torch.arange(T, device=DEV) * 5 // T - 1).to(torch.int32)
     want = moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"])
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -162,6 +165,26 @@ def test_repeats_bit_for_bit_on_streams_and_graphs():
     ids.copy_(ids.flip(0))
     g.replay()
     assert torch.equal(out, moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"]))
+
+
+@pytest.mark.parametrize("T", [5, 300, 2900])
+def test_no_adapter_at_all(T):
+    d = make(T, 256, 192, 16, 2, seed=1)
+    ids = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    assert torch.equal(moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"]), d["y"])
+
+
+def test_many_runs_agree():
+    """The same call many times, with other calls between: every run the same bits."""
+    a = make(4096, 2048, 512, 16, 12, seed=5)
+    b = make(3100, 640, 2048, 64, 3, seed=6)
+    ida = (torch.arange(4096, device=DEV) * 13 // 4096 - 1).to(torch.int32)
+    idb = torch.randint(-1, 3, (3100,), generator=torch.Generator(DEV).manual_seed(1), device=DEV).to(torch.int32)
+    run = lambda d, i: moe.add_adapters(d["x"], d["y"], i, d["a"], d["b"], d["scales"])
+    wa, wb = run(a, ida), run(b, idb)
+    for _ in range(40):
+        ga, gb = run(a, ida), run(b, idb)
+        assert torch.equal(ga, wa) and torch.equal(gb, wb)
 
 
 def test_no_tokens():
