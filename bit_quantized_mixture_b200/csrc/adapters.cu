@@ -31,8 +31,9 @@ constexpr int kAdTokenMax = 256, kAdTokenWork = 8192;        // most tokens, mos
 constexpr int kAdCluster8 = 32, kAdCluster4 = 192;           // up to so many tokens 8, 4 CTAs
 // Tiles of 16 against 64 tokens: 1024 tokens rank 16 8.7 / 12 us, 4096 tokens 29 / 25;
 // tiles of 128 on tcgen05 (adapters_tc.cu) against those: 2048 tokens rank 16 22 / 15,
-// 4096 tokens 24 / 25, 8192 tokens rank 64 40 / 59.
-constexpr int kAdSmallTile = 2048, kAdTcMin = 2800;
+// 4096 tokens 24 / 25, 8192 tokens rank 64 40 / 59; with fp32 outputs (three parts of
+// z) 4096 tokens rank 16 34 / 32, 8192 tokens 52 / 54, rank 64 72 / 81.
+constexpr int kAdSmallTile = 2048, kAdTcMin = 2800, kAdTcMinWide = 8192;
 constexpr int kAdThreads = 256;
 
 MOE_DEV float dot8(const uint4& p, const uint4& q, float s) {
@@ -195,8 +196,9 @@ MOE_DEV void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
 // results are, without any exchange, the first operand of step 2 with B's
 // 16-byte loads.
 //
-// RG: groups of 32 rank rows.  WIDE: y and out fp32; z is then held as two bf16
-// halves (16 significant bits), as one otherwise.
+// RG: groups of 32 rank rows.  z is held in bf16 (half a step 2^-8 of a term that
+// is then rounded into a bf16 output); WIDE, y and out fp32: in three bf16 parts,
+// 24 significant bits (two left 1.6e-6 of the output, sixteen times fp32's error).
 constexpr int kTileCluster = 4;
 constexpr int kTileWarps = 8;
 
@@ -210,6 +212,7 @@ template <int RG, int MT, int MG, bool WIDE>
 __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_tile(const __grid_constant__ AdapterArgs a) {
     constexpr int BT = 16 * MT * MG, PARTS = kTileWarps / MG, TJ = 4 * RG, NPASS = RG == 4 ? 2 : 1, PJ = TJ / NPASS;
     constexpr int ZN = MG * MT * TJ * 2 * 32;             // float2 values of z
+    constexpr int ZPARTS = WIDE ? 3 : 1;                  // bf16 parts that z is held in
     extern __shared__ __align__(16) float2 part_s[];      // [PARTS][ZN]; later zf in place of part 1 on
     __shared__ float s_scale[BT];
     cg::cluster_group cl = cg::this_cluster();
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
     }
     cl.sync();
     // z * scale as the second product's first operand: [MG][MT][2 RG steps][32
-    // lanes][4 words], for WIDE the low halves behind it
+    // lanes][4 words] for each of its parts
     uint32_t* zf = reinterpret_cast<uint32_t*>(part_s + ZN);
     for (int i = threadIdx.x; i < ZN; i += kTileWarps * 32) {
         float2 v = make_float2(0.0f, 0.0f);
@@ -322,10 +325,14 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
         const float sc = s_scale[16 * mm + 8 * h + (l >> 2)];
         v.x *= sc;
         v.y *= sc;
-        const uint32_t hi = pack_bf16x2(v.x, v.y);
         const int w = ((mm * 2 * RG + (j >> 1)) * 32 + l) * 4 + (j & 1) * 2 + h;
-        zf[w] = hi;
-        if (WIDE) zf[ZN + w] = pack_bf16x2(v.x - bf16_lo(hi), v.y - bf16_hi(hi));
+#pragma unroll
+        for (int q = 0; q < ZPARTS; ++q) {
+            const uint32_t p = pack_bf16x2(v.x, v.y);
+            zf[q * ZN + w] = p;
+            v.x -= bf16_lo(p);
+            v.y -= bf16_hi(p);
+        }
     }
     // the others may still read this CTA's sums: waited for at the end
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -381,8 +388,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int lowhalf = 0; lowhalf < (WIDE ? 2 : 1); ++lowhalf) {
-                            const uint4* zp = zq + (size_t)(m * 2 * RG + 2 * G) * 32 + lowhalf * (ZN / 4);
+                        for (int q = ZPARTS - 1; q >= 0; --q) {
+                            const uint4* zp = zq + (size_t)(m * 2 * RG + 2 * G) * 32 + q * (ZN / 4);
                             const uint4 z0 = zp[0], z1 = zp[32];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -469,7 +476,7 @@ cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st) {
         if (a.T <= kAdCluster8) return launch_tokens<8>(a, st);
         return a.T <= kAdCluster4 ? launch_tokens<4>(a, st) : launch_tokens<2>(a, st);
     }
-    if (a.T >= kAdTcMin) {
+    if (a.T >= (a.wide ? kAdTcMinWide : kAdTcMin)) {
         const cudaError_t e = launch_add_adapters_tc(a, st);
         if (e != cudaErrorNotSupported) return e;
     }

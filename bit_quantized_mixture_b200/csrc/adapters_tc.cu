@@ -21,8 +21,8 @@
 //
 // A row's results come from its own adapter's accumulators alone, so weights that
 // are not finite spoil no other adapter's tokens.  z is held in bf16 (half a step
-// 2^-8 of a term that is then rounded into a bf16 output), for fp32 outputs in two
-// bf16 halves (2^-16).
+// 2^-8 of a term that is then rounded into a bf16 output), for fp32 outputs in three
+// bf16 parts (24 significant bits).
 //
 // Warps: 0 loads x and y, 11-12 A and B (TMA; one thread for all of it spends longer on
 // its waits and loads than a chunk takes), 1-2 MMA issuers, 3-10 epilogue (two groups
@@ -69,7 +69,8 @@ struct TcCfg {
     static constexpr int OFF_Z = OFF_SMALL + kTcStreams * NSMALL * SMALL;        // fp32 sums of the rows that this CTA owns, by source CTA
     static constexpr int ZBLOCK = kTcRows * 128;                    // 64 columns of the bf16 operand
     static constexpr int OFF_OP = OFF_Z + RB * 64 * kTcRows * 4;
-    static constexpr size_t BYTES = OFF_OP + RB * (WIDE ? 2 : 1) * ZBLOCK + 1024;   // base rounded up to the swizzle's 1024
+    static constexpr int PARTS = WIDE ? 3 : 1;                      // bf16 parts that z is held in
+    static constexpr size_t BYTES = OFF_OP + RB * PARTS * ZBLOCK + 1024;   // base rounded up to the swizzle's 1024
 };
 
 struct TcMaps {
@@ -361,7 +362,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                     tc_fence_after();
                     const uint64_t bd = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
                     const uint32_t dst = tmem + kTcZCols + 64u * (uint32_t)(w * kTcDBufs + buf);
-                    for (int h = 0; h < (WIDE ? 2 : 1); ++h)
+                    for (int h = 0; h < C::PARTS; ++h)
                         for (int q = 0; q < steps; ++q)
                             mma_bf16(dst, dz + (uint64_t)((h * RB + (q >> 2)) * (C::ZBLOCK >> 4) + 2 * (q & 3)),
                                      bd + (uint64_t)((q >> 2) * (NC * 128 >> 4) + 2 * (q & 3)), ido, h + q > 0 ? 1u : 0u);
@@ -487,16 +488,17 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
 #pragma unroll
                         for (int q = 0; q < 8; ++q) z[q] = 8 * j + q < rank ? z[q] * scale : 0.0f;
                     }
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        hi[q] = pack_bf16x2(z[2 * q], z[2 * q + 1]);
-                        lo[q] = pack_bf16x2(z[2 * q] - bf16_lo(hi[q]), z[2 * q + 1] - bf16_hi(hi[q]));
-                    }
                     uint8_t* d = op + (j >> 3) * C::ZBLOCK + sw_piece(r, j & 7);
-                    for (int q = 0; q < CL; ++q) {
-                        st_cluster_v4(d, q, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                        if (WIDE) st_cluster_v4(d + RB * C::ZBLOCK, q, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+                    for (int h = 0; h < C::PARTS; ++h, d += RB * C::ZBLOCK) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            w[q] = pack_bf16x2(z[2 * q], z[2 * q + 1]);
+                            z[2 * q] -= bf16_lo(w[q]);
+                            z[2 * q + 1] -= bf16_hi(w[q]);
+                        }
+                        for (int q = 0; q < CL; ++q) st_cluster_v4(d, q, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
                 asm volatile("fence.proxy.async;" ::: "memory");

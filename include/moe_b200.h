@@ -369,7 +369,7 @@ typedef struct {
  * fp32; out may be y itself (same ld) and otherwise overlaps no input.
  * Products and sums are fp32, out is rounded once.  With more than a few
  * tokens the second product's operand, scale * a x, is held in bf16 for bf16
- * outputs and in two bf16 halves (16 significant bits) for fp32 outputs.
+ * outputs and in three bf16 parts (24 significant bits) for fp32 outputs.
  * Deterministic; needs no workspace.
  * Errors: INVALID_ARG, UNSUPPORTED (R, K or N), CUDA. */
 moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,
