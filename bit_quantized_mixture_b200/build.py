@@ -1,4 +1,5 @@
-"""Build the CUDA library libmoe_b200.so in-tree with nvcc for sm_100a.
+"""Build the CUDA library libmoe_b200.so in-tree with nvcc for sm_100a, and the
+Python extension _binding.so (csrc/binding.cpp) against it.
 
     python -m bit_quantized_mixture_b200.build [--force] [--verbose]
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 INCLUDE = os.path.join(ROOT, "include")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -50,6 +54,18 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_command(target):
+    """g++ command of the Python extension (host code; tensors through torch's C++ headers)."""
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += ["-I" + INCLUDE, "-isystem", os.path.join(troot, "include"), "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include")]
+    cmd += ["-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd += [BINDING_SRC, "-o", target, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    cmd += ["-L" + os.path.join(troot, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return cmd
+
+
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -77,6 +93,11 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         cmd = [cc] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs + ["-lcudart"]
         run(cmd)
         os.replace(LIB + ".tmp", LIB)
+    # the entry points' declarations and the extension's own source (the library
+    # is found by name when it is loaded)
+    if force or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "moe_b200.h"), __file__]):
+        run(binding_command(BINDING + ".tmp"))
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import numpy as np
 import torch
@@ -156,7 +155,7 @@ def _refuse(msg):
     raise MoeError(MOE_ERR_INVALID_ARG, msg)
 
 
-_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_BF16 = (torch.bfloat16,)
 _BF16_F32 = (torch.bfloat16, torch.float32)
 
 
@@ -180,28 +179,27 @@ def _rows(name, t, dtypes, T, W, dev):
     return t.data_ptr(), s0 if T > 1 else W
 
 
-def _lead(name, t, dtypes):
-    """(T, W, device number) of the 2-D CUDA tensor that sets a call's sizes."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda:
-        _refuse(f"{name}: need a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    T, W = t.shape
-    return T, W, t.get_device()
+def _raw(stream):
+    """A stream object's (or raw) handle; None stays None: torch's current stream."""
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with device number dev current, on its current stream
-    when none is given."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, stream)
-    if status != MOE_OK:
-        _check(status)
+_ext = None
+
+
+def binding():
+    """The Python extension with the tensor checks of the calls below; raise if
+    it is not built."""
+    global _ext
+    if _ext is None:
+        lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing: build it with python -m bit_quantized_mixture_b200.build") from e
+        _binding.init(MoeError)
+        _ext = _binding
+    return _ext
 
 
 def _new(shape, dtype, dev, stream):
@@ -227,21 +225,24 @@ class Routing:
         self.E = None if bias is None else bias.shape[0]
         self.c = RoutingRule(SCORE[score], num_groups, top_groups, GROUP_SCORE[group_score], int(bool(renorm)), scale,
                              _cuda("bias", bias, torch.float32, (self.E,), None) if bias is not None else None)
+        self.address = ctypes.addressof(self.c)
+
+
+def _device(name, t):
+    """The device number of a CUDA tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(f"{name}: need a CUDA tensor")
+    return t.get_device()
 
 
 def select_experts(logits, k, rule, ids=None, w=None, stream=None):
     """fp32 logits [T, E] -> (ids int32 [T, k], weights fp32 [T, k]) under a
     Routing rule (moe_select_experts)."""
-    T, E, dev = _lead("logits", logits, _F32)
-    ptr, ld = _rows("logits", logits, _F32, T, E, dev)
-    if rule.bias is not None and (rule.E != E or rule.bias.get_device() != dev):
-        _refuse(f"bias: need {E} entries on cuda:{dev}")
     if ids is None:
-        ids = _new((T, k), torch.int32, dev, stream)
+        ids = _new((logits.shape[0], k), torch.int32, _device("logits", logits), stream)
     if w is None:
-        w = _new((T, k), torch.float32, dev, stream)
-    _call(lib().moe_select_experts, dev, stream, ptr, ld, T, E, k, rule.c,
-          _cuda("ids", ids, torch.int32, (T, k), dev), _cuda("w", w, torch.float32, (T, k), dev))
+        w = _new((logits.shape[0], k), torch.float32, _device("logits", logits), stream)
+    binding().select_experts(logits, k, rule.address, rule.bias, ids, w, _raw(stream))
     return ids, w
 
 
@@ -260,18 +261,9 @@ def add_adapters(x, y, adapter_ids, a, b, scales, ranks=None, out=None, stream=N
     (moe_add_adapters): x bf16 [T, K], y bf16 or fp32 [T, N], a bf16
     [n, R, K], b bf16 [n, N, R], scales fp32 [n], ranks int32 [n] or None.
     out may be y; by default it is a new tensor."""
-    T, K, dev = _lead("x", x, _BF16)
-    c = _adapter_set(a, b, scales, ranks, dev)
-    N = c.N
-    if c.K != K:
-        _refuse(f"a: {c.K} columns, x has {K}")
-    xp, ldx = _rows("x", x, _BF16, T, K, dev)
-    yp, ldy = _rows("y", y, _BF16_F32, T, N, dev)
     if out is None:
-        out = _new((T, N), y.dtype, dev, stream)
-    op, ldo = (yp, ldy) if out is y else _rows("out", out, (y.dtype,), T, N, dev)
-    _call(lib().moe_add_adapters, dev, stream, xp, ldx, yp, ldy, op, ldo, y.dtype is torch.float32, T,
-          _cuda("adapter_ids", adapter_ids, torch.int32, (T,), dev), c)
+        out = _new(tuple(y.shape), y.dtype, _device("y", y), stream)
+    binding().add_adapters(x, y, adapter_ids, a, b, scales, ranks, out, _raw(stream))
     return out
 
 
@@ -286,35 +278,21 @@ def _gate(gate, T, H, dev):
     return GATE["channel"], _cuda("gate", gate, torch.bfloat16, (H,), dev), 0
 
 
-_NORM = struct.Struct("@7P5q6i3f4x")
-
-
 def block_norm(r, y=None, post_weight=None, gate=None, gate_sigmoid=False, pre_weight=None, eps=1e-6, branch_scale=1.0,
                residual_scale=1.0, unit_offset=False, r_out=None, x_out=None, stream=None):
     """The norms, gate and residual add between two blocks (moe_block_norm):
     r bf16 or fp32 [T, H], y bf16 [T, H], weights bf16 [H]; gate bf16 [H]
     (channel), fp32 [T] (token) or bf16 [T, H] (element).  Returns (r', x);
     x is None without pre_weight.  r_out may be r, x_out may be y."""
-    T, H, dev = _lead("r", r, _BF16_F32)
-    rp, ldr = _rows("r", r, _BF16_F32, T, H, dev)
-    yp, ldy = _rows("y", y, _BF16, T, H, dev) if y is not None else (0, 0)
-    wpost = _cuda("post_weight", post_weight, torch.bfloat16, (H,), dev) if post_weight is not None else 0
-    kind, gp, ldg = _gate(gate, T, H, dev)
     if r_out is None:
-        r_out = _new((T, H), r.dtype, dev, stream)
-    rop, ldro = (rp, ldr) if r_out is r else _rows("r_out", r_out, (r.dtype,), T, H, dev)
-    wpre = xop = ldx = 0
-    if pre_weight is not None:
-        wpre = _cuda("pre_weight", pre_weight, torch.bfloat16, (H,), dev)
-        if x_out is None:
-            x_out = _new((T, H), torch.bfloat16, dev, stream)
-        xop, ldx = _rows("x_out", x_out, _BF16, T, H, dev)
-    elif x_out is not None:
+        r_out = _new(tuple(r.shape), r.dtype, _device("r", r), stream)
+    if x_out is None:
+        if pre_weight is not None:
+            x_out = _new(tuple(r.shape), torch.bfloat16, _device("r", r), stream)
+    elif pre_weight is None:
         _refuse("x_out: needs pre_weight")
-    n = Norm.from_buffer_copy(_NORM.pack(rp, yp, wpost, gp, wpre, rop, xop, ldr, ldy, ldg, ldro, ldx, T, H,
-                                         r.dtype is torch.float32, kind, bool(gate_sigmoid), bool(unit_offset), eps,
-                                         branch_scale, residual_scale))
-    _call(lib().moe_block_norm, dev, stream, n)
+    binding().block_norm(r, y, post_weight, gate, gate_sigmoid, pre_weight, eps, branch_scale, residual_scale, unit_offset, r_out, x_out,
+                         _raw(stream))
     return r_out, x_out
 
 
