@@ -141,6 +141,9 @@ MOE_DEV void wait_some(uint64_t* bar, uint32_t parity) {
     for (int q = 0; q < 1000 && !mbar_try_wait(bar, parity); ++q) {}
 }
 
+// where a call without an error word of its own records a wait that gave up
+__device__ int g_wait_err;
+
 template <int RB, bool WIDE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMaps maps, int rows_a, int per_pass) {
@@ -159,6 +162,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
     // the swizzle and its descriptors count from 1024-byte boundaries
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     cg::cluster_group cl = cg::this_cluster();
+    int* const err = a.err ? a.err : &g_wait_err;
     const int CL = (int)cl.num_blocks(), crank = (int)cl.block_rank();
     const int t0 = (int)(blockIdx.x / CL) * kTcRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -260,7 +264,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                 Ring<NBIG>& r = ring[i & (kTcStreams - 1)];
                 const int w = i & (kTcStreams - 1);
                 if (!out) {
-                    ok = mbar_wait(&big_empty[w][r.slot], r.phase ^ 1u, &abort_flag, a.err, 41);
+                    ok = mbar_wait(&big_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 41);
                     if (!ok) return;
                     mbar_arrive_expect_tx(&big_full[w][r.slot], C::BIG);
                     tma_load_2d(smem + (w * NBIG + r.slot) * C::BIG, map, col, t0, &big_full[w][r.slot]);
@@ -295,7 +299,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                 for (int i = 0; ok && i < k1 - k0; ++i, kc.next()) {
                     if ((i & (kTcStreams - 1)) != w) continue;
                     for (int d = d0; d < d1; ++d, r.next()) {
-                        if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, a.err, 42))) break;
+                        if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 42))) break;
                         mbar_arrive_expect_tx(&small_full[w][r.slot], (uint32_t)rows_a * 128u);
                         tma_load_3d(slots + r.slot * C::SMALL, &maps.a, 64 * kc.at, 0, s_list[d], &small_full[w][r.slot]);
                     }
@@ -305,7 +309,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             for (int i = 0; ok && i < n1 - n0; ++i, nc.next()) {
                 if ((i & (kTcStreams - 1)) != w) continue;
                 for (int d = 0; d < D; ++d, r.next()) {
-                    if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, a.err, 44))) break;
+                    if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 44))) break;
                     const int nb = (s_rank[d] + 63) / 64;
                     mbar_arrive_expect_tx(&small_full[w][r.slot], (uint32_t)(nb * NC * 128));
                     for (int b = 0; b < nb; ++b)
@@ -331,13 +335,13 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             const uint32_t idz = idesc_bf16_f32(kTcRows, rows_a), ido = idesc_bf16_f32(kTcRows, NC);
             for (int p = 0; ok && p < passes; ++p) {
                 const int nd = min(D - p * per_pass, per_pass);
-                if (p > 0 && !(ok = mbar_wait(&z_free, (uint32_t)(p - 1) & 1u, &abort_flag, a.err, 45))) break;
+                if (p > 0 && !(ok = mbar_wait(&z_free, (uint32_t)(p - 1) & 1u, &abort_flag, err, 45))) break;
                 tc_fence_after();
                 for (int kc = k0 + w; ok && kc < k1; kc += kTcStreams, big.next()) {
-                    if (!(ok = mbar_wait(&big_full[w][big.slot], big.phase, &abort_flag, a.err, 46))) break;
+                    if (!(ok = mbar_wait(&big_full[w][big.slot], big.phase, &abort_flag, err, 46))) break;
                     const uint64_t xd = dx + (uint64_t)(big.slot * (C::BIG >> 4));
                     for (int d = 0; d < nd; ++d, small.next()) {
-                        if (!(ok = mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, a.err, 47))) break;
+                        if (!(ok = mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, err, 47))) break;
                         const uint64_t ad = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
                         const uint32_t dst = tmem + (uint32_t)((d * kTcStreams + w) * rows_a);
 #pragma unroll
@@ -349,15 +353,15 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                 if (ok && w < k1 - k0) mma_commit(&z_full);
             }
             if (ok && D > 0) {
-                ok = mbar_wait_cluster(&op_full, 0u, &abort_flag, a.err, 48);
+                ok = mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 48);
                 fence_proxy_async_smem();            // the operand came by ordinary stores
             }
             for (int nc = n0 + w; ok && nc < n1; nc += kTcStreams)
                 for (int d = 0; d < D; ++d, small.next(), ++unit) {
                     const int buf = unit & 1, steps = (s_rank[d] + 15) / 16;
-                    ok = a.ranks ? mbar_wait(&small_clean[w][small.slot], (uint32_t)(unit / NSMALL) & 1u, &abort_flag, a.err, 49)
-                                 : mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, a.err, 49);
-                    ok = ok && mbar_wait(&d_empty[w][buf], ((uint32_t)(unit >> 1) & 1u) ^ 1u, &abort_flag, a.err, 50);
+                    ok = a.ranks ? mbar_wait(&small_clean[w][small.slot], (uint32_t)(unit / NSMALL) & 1u, &abort_flag, err, 49)
+                                 : mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, err, 49);
+                    ok = ok && mbar_wait(&d_empty[w][buf], ((uint32_t)(unit >> 1) & 1u) ^ 1u, &abort_flag, err, 50);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t bd = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
@@ -381,7 +385,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             bool ok = true;
             for (int i = 0; ok && i < n1 - n0; ++i, at.next()) {
                 const int w = i & (kTcStreams - 1), s = ring[w].slot;
-                if (!(ok = mbar_wait(&chunk_done[w][s], ring[w].phase, &abort_flag, a.err, 59))) break;
+                if (!(ok = mbar_wait(&chunk_done[w][s], ring[w].phase, &abort_flag, err, 59))) break;
                 tma_store_2d(&maps.out, NC * at.at, t0, smem + (w * NBIG + s) * C::BIG);
                 bulk_commit();
                 bulk_wait_read<0>();
@@ -399,14 +403,14 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         if (a.ranks) {
             // the first product's uses of the slots are over then, and the slots
             // go on where it left off
-            bool ok = D == 0 || __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, a.err, 57));
+            bool ok = D == 0 || __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 57));
             int used[kTcStreams];
             for (int w = 0; w < kTcStreams; ++w) used[w] = D * count(k0, k1, w);
             for (int nc = n0; ok && nc < n1; ++nc) {
                 const int w = (nc - n0) & (kTcStreams - 1);
                 for (int d = 0; d < D; ++d, ++used[w]) {
                     const int slot = used[w] % NSMALL;
-                    if (!(ok = all_wait(&small_full[w][slot], (uint32_t)(used[w] / NSMALL) & 1u, &abort_flag, a.err, 56))) break;
+                    if (!(ok = all_wait(&small_full[w][slot], (uint32_t)(used[w] / NSMALL) & 1u, &abort_flag, err, 56))) break;
                     const int rank = s_rank[d], steps = (rank + 15) / 16;
                     if (rank & 15) {
                         uint8_t* bt = smem + C::OFF_SMALL + (w * NSMALL + slot) * C::SMALL;
@@ -437,7 +441,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             const int own_rows = kTcRows / CL, owner = row / own_rows, quads = rows_a / 4;
             float4* zp = reinterpret_cast<float4*>(smem + C::OFF_Z);
             for (int p = 0; ok && p < passes; ++p) {
-                if (!(ok = all_wait(&z_full, (uint32_t)p & 1u, &abort_flag, a.err, 51))) break;
+                if (!(ok = all_wait(&z_full, (uint32_t)p & 1u, &abort_flag, err, 51))) break;
                 tc_fence_after();
                 const int nd = min(D - p * per_pass, per_pass);
                 for (int d = 0; d < nd; ++d) {
@@ -469,7 +473,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             __syncwarp();
             if (ok) {
                 if (lane < CL) mbar_arrive_cluster(&z_ready, lane);
-                ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_ready, 0u, &abort_flag, a.err, 52));
+                ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_ready, 0u, &abort_flag, err, 52));
             }
             if (ok) {
                 uint8_t* op = smem + C::OFF_OP;
@@ -509,15 +513,15 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         // The first product's uses of the slots are over (a parity tells only one
         // use from the next), and this group's chunks, every other one, go on
         // where its stream left off.
-        if (D == 0) ok = all_wait(&z_full, 0u, &abort_flag, a.err, 58);
+        if (D == 0) ok = all_wait(&z_full, 0u, &abort_flag, err, 58);
         int unit = 0, big = passes * count(k0, k1, group);
         for (int nc = n0 + group; ok && nc < n1; nc += kTcStreams, ++big) {
             const int s = big % NBIG;
-            if (!(ok = all_wait(&big_full[group][s], (uint32_t)(big / NBIG) & 1u, &abort_flag, a.err, 54))) break;
+            if (!(ok = all_wait(&big_full[group][s], (uint32_t)(big / NBIG) & 1u, &abort_flag, err, 54))) break;
             uint8_t* tile = smem + (group * NBIG + s) * C::BIG;
             for (int d = 0; d < D; ++d, ++unit) {
                 const int buf = unit & 1;
-                if (!(ok = all_wait(&d_full[group][buf], (uint32_t)(unit >> 1) & 1u, &abort_flag, a.err, 55))) break;
+                if (!(ok = all_wait(&d_full[group][buf], (uint32_t)(unit >> 1) & 1u, &abort_flag, err, 55))) break;
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, mine == d)) {
                     const uint32_t src = tmem + lane_base + kTcZCols + 64u * (uint32_t)(group * kTcDBufs + buf);
@@ -638,6 +642,13 @@ cudaError_t launch_tc(const AdapterArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t take_wait_error(int* code) {
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_wait_err, sizeof(int));
+    const int zero = 0;
+    if (e == cudaSuccess && *code) e = cudaMemcpyToSymbol(g_wait_err, &zero, sizeof(int));
+    return e;
+}
 
 cudaError_t launch_add_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
     if (a.R <= 64) return a.wide ? launch_tc<1, true>(a, st) : launch_tc<1, false>(a, st);

@@ -87,6 +87,8 @@ struct AdapterArgs {
 // adapters_tc.cu: tiles of 128 tokens on the tensor cores (cudaErrorNotSupported:
 // a tensor that no tensor map describes)
 cudaError_t launch_add_adapters_tc(const AdapterArgs& a, cudaStream_t st);
+// the code of a bounded wait that gave up in a call without an error word (0: none), and clears it
+cudaError_t take_wait_error(int* code);
 cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st);
 
 // block_norm.cu

@@ -1021,6 +1021,15 @@ moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t 
     return MOE_OK;
 }
 
+moe_status moe_adapters_status(moe_stream_t stream) {
+    cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+    int code = 0;
+    if (e == cudaSuccess) e = take_wait_error(&code);
+    if (e != cudaSuccess) return cuda_fail(nullptr, e, "moe_adapters_status");
+    if (code) return fail(nullptr, MOE_ERR_TIMEOUT, "moe_add_adapters gave up a bounded wait (site %d); its outputs are invalid", code);
+    return MOE_OK;
+}
+
 // the arguments of moe_block_norm (h: whose error text a failure sets)
 static moe_status check_norm(moe_layer* h, const char* fn, const moe_norm* n) {
     if (n->H < 8 || n->H % 8 || n->H > 16384)

@@ -24,7 +24,13 @@ namespace moe {
 
 namespace {
 
-constexpr int kSelWarps = 4;         // warps (tokens) of a CTA
+constexpr int kSelWarps = 4;         // warps of a CTA
+// Up to so many tokens (four per SM) a CTA per token, whose four warps walk through
+// a quarter of its long way of instructions each, then a warp per token.  us, CTA /
+// warp per token: 1 token of 512 experts in 8 groups 3.9 / 5.2, 333 of 600 in 24
+// groups 6.1 / 9.6, 600 tokens 8.5 / 11.6 and (512 in 8 groups) 6.0 / 6.5; 1200 tokens
+// 7.0 / 6.8, 2400 10.8 / 8.6.
+constexpr int kSelTeamTokens = 592;
 constexpr int kSelCand = 64;         // candidates that a warp's list holds
 constexpr int kSelSpare = 4;         // ... and may hold beyond k of the lanes' largest keys
 
@@ -70,6 +76,16 @@ MOE_DEV void store_weights(const SelectArgs& a, int t, int id, float x, bool on,
         a.w[(size_t)t * a.k + lane] = w * a.scale;
     }
 }
+
+// what the W warps of a token tell one another
+template <int W>
+struct SelTeam {
+    float top[W], sum[W];
+    int count[W];
+    float2 largest[W][32];
+    unsigned kept;
+    bool fail;
+};
 
 // sum of exp(l - top) over the eligible experts in fp64 (softmax)
 MOE_DEV double softmax_total(const SelectArgs& a, const float* row, float top) {
@@ -315,9 +331,77 @@ __device__ __noinline__ int group_rank_exact(const SelectArgs& a, const float* r
     return rank;
 }
 
-// The rule in fp32 for one token, one warp; lane l holds the experts
-// 128 i + 4 ((l + 9 i) % 32) + q in v[4 i + q] (turned from chunk to chunk, so
-// that the groups that stay are not all in a few lanes).  Group scores, and then keys, that are nearer
+// The groups that stay, as a mask of the lanes that speak for them (group g's
+// first: g << group_lanes_log2); fail: group_rank_exact could not tell.  One warp.
+template <bool VEC>
+MOE_DEV unsigned choose_groups(const SelectArgs& a, const float* row, float top, const float* gkey, float ks, bool scored, bool top2,
+                               SelScratch& sc, bool& fail) {
+    const int lane = threadIdx.x & 31;
+    const unsigned all = 0xffffffffu;
+    // 2^gl lanes per group, their largest two keys folded together; each
+    // group starts at another offset so that the lanes' banks differ
+    const int gl = a.group_lanes_log2, L = 1 << gl;
+    const int g = lane >> gl, sub = lane & (L - 1);
+    float b1 = -INFINITY, b2 = -INFINITY;
+    auto take = [&](float x) {
+        b2 = fmaxf(b2, fminf(b1, x));
+        b1 = fmaxf(b1, x);
+    };
+    if (g < a.G) {
+        const bool quads = VEC && (a.per & 3) == 0;
+        const int m = quads ? a.per >> 2 : a.per, nit = (m + L - 1) >> gl;
+        int it = g % nit;
+        if (quads) {
+#pragma unroll 4
+            for (int n = 0; n < nit; ++n) {
+                const int j = sub + (it << gl);
+                const float4 x = j < m ? *reinterpret_cast<const float4*>(gkey + g * a.per + 4 * j)
+                                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                take(x.x); take(x.y); take(x.z); take(x.w);
+                it = it + 1 == nit ? 0 : it + 1;
+            }
+        } else {
+#pragma unroll 4
+            for (int n = 0; n < nit; ++n) {
+                const int j = sub + (it << gl);
+                take(j < m ? gkey[g * a.per + j] : -INFINITY);
+                it = it + 1 == nit ? 0 : it + 1;
+            }
+        }
+    }
+    __syncwarp();
+    for (int o = L >> 1; o > 0; o >>= 1) {
+        const float c1 = __shfl_xor_sync(all, b1, o), c2 = __shfl_xor_sync(all, b2, o);
+        b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+        b1 = fmaxf(b1, c1);
+    }
+    const float mine = top2 && b2 > -INFINITY ? b1 + b2 : b1;
+    // rank of this lane's group: lane g << gl speaks for group g
+    int rank = 0;
+#pragma unroll 4
+    for (int q = 0; q < a.G; ++q) {
+        const float x = __shfl_sync(all, mine, q << gl);
+        rank += (x > mine || (x == mine && q < g)) ? 1 : 0;
+    }
+    const bool speaks = g < a.G && sub == 0;
+    if (scored && a.keep < a.G) {
+        // the last group that stays against the first that does not: errors
+        // of up to two keys and their sum, at most the largest group score's
+        const float big = warp_max(speaks && mine > -INFINITY ? fmaxf(fabsf(b1), fabsf(mine)) : 0.0f);
+        const float in = warp_max(speaks && rank == a.keep - 1 ? mine : -INFINITY);
+        const float out = warp_max(speaks && rank == a.keep ? mine : -INFINITY);
+        if (out > -INFINITY && !(in - out > 4.2f * ks + 7.5e-7f * big)) {
+            rank = group_rank_exact(a, row, top, gkey, b1, b2, ks, sc);
+            fail = rank < 0;
+        }
+    }
+    return __ballot_sync(all, speaks && rank < a.keep);
+}
+
+// The rule in fp32 for one token, W warps; lane l of warp w holds the experts
+// 128 c + 4 ((l + 9 c) % 32) + q of chunk c = W i + w in v[4 i + q] (turned from
+// chunk to chunk, so that the groups that stay are not all in a few lanes).  With
+// W > 1 warp 0 alone chooses the groups and ranks the candidates.  Group scores, and then keys, that are nearer
 // than their errors are taken again in fp64.  false: the candidates are more
 // than the list holds, or fewer than k; nothing is written.
 //
@@ -335,13 +419,20 @@ __device__ __noinline__ int group_rank_exact(const SelectArgs& a, const float* r
 // k + 4 of them: about 15 candidates of 512 for k = 10 and 40 of 1024 for
 // k = 32 (one key per lane would leave 130 there).  The candidates go to the
 // warp's list and each is ranked by counting those ahead of it.
-template <int CH, bool VEC>
-MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey) {
+template <int CH, bool VEC, int W>
+MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey, SelTeam<W>& team) {
     constexpr int SLOTS = 4 * CH;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, wid = W > 1 ? (int)threadIdx.x >> 5 : 0;
+    auto sync = [] {
+        if (W > 1) __syncthreads();
+        else __syncwarp();
+    };
     const unsigned all = 0xffffffffu;
     const float* row = a.logits + (size_t)t * a.ld;
-    auto first = [&](int i) { return 128 * i + 4 * ((lane + 9 * i) & 31); };
+    auto first = [&](int i) {
+        const int c = W * i + wid;
+        return 128 * c + 4 * ((lane + 9 * c) & 31);
+    };
     // four consecutive floats from p[e], off: what stands for entries past E
     auto load4 = [&](const float* p, int e, float off, float* d) {
         if (VEC) {
@@ -374,9 +465,20 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) top = fmaxf(top, v[i]);
         top = warp_max(top);
+        if (W > 1) {
+            if (lane == 0) team.top[wid] = top;
+            sync();
+            for (int w = 0; w < W; ++w) top = fmaxf(top, team.top[w]);
+        }
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) s += __expf(v[i] - top);     // 0 for those that are off
         total = warp_sum(s);
+        if (W > 1) {
+            if (lane == 0) team.sum[wid] = total;
+            sync();
+            total = 0.0f;
+            for (int w = 0; w < W; ++w) total += team.sum[w];
+        }
         // without a bias the groups compare exp(l - top) itself, total times the scores
         ks = a.bias ? __fdividef(5e-6f, total) : 5e-6f;
     }
@@ -412,67 +514,19 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
                     if (e + q < a.E) gkey[e + q] = g[q];
             }
         }
-        __syncwarp();
+        sync();
     }
     if (a.G > 1) {
-        // 2^gl lanes per group, their largest two keys folded together; each
-        // group starts at another offset so that the lanes' banks differ
-        const int gl = a.group_lanes_log2, L = 1 << gl;
-        const int g = lane >> gl, sub = lane & (L - 1);
-        float b1 = -INFINITY, b2 = -INFINITY;
-        auto take = [&](float x) {
-            b2 = fmaxf(b2, fminf(b1, x));
-            b1 = fmaxf(b1, x);
-        };
-        if (g < a.G) {
-            const bool quads = VEC && (a.per & 3) == 0;
-            const int m = quads ? a.per >> 2 : a.per, nit = (m + L - 1) >> gl;
-            int it = g % nit;
-            if (quads) {
-#pragma unroll 4
-                for (int n = 0; n < nit; ++n) {
-                    const int j = sub + (it << gl);
-                    const float4 x = j < m ? *reinterpret_cast<const float4*>(gkey + g * a.per + 4 * j)
-                                           : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                    take(x.x); take(x.y); take(x.z); take(x.w);
-                    it = it + 1 == nit ? 0 : it + 1;
-                }
-            } else {
-#pragma unroll 4
-                for (int n = 0; n < nit; ++n) {
-                    const int j = sub + (it << gl);
-                    take(j < m ? gkey[g * a.per + j] : -INFINITY);
-                    it = it + 1 == nit ? 0 : it + 1;
-                }
-            }
+        const int gl = a.group_lanes_log2;
+        bool fail = false;
+        unsigned kept = wid == 0 ? choose_groups<VEC>(a, row, top, gkey, ks, scored, top2, sc, fail) : 0u;
+        if (W > 1) {
+            if (wid == 0 && lane == 0) { team.kept = kept; team.fail = fail; }
+            sync();
+            kept = team.kept;
+            fail = team.fail;
         }
-        __syncwarp();
-        for (int o = L >> 1; o > 0; o >>= 1) {
-            const float c1 = __shfl_xor_sync(all, b1, o), c2 = __shfl_xor_sync(all, b2, o);
-            b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
-            b1 = fmaxf(b1, c1);
-        }
-        const float mine = top2 && b2 > -INFINITY ? b1 + b2 : b1;
-        // rank of this lane's group: lane g << gl speaks for group g
-        int rank = 0;
-#pragma unroll 4
-        for (int q = 0; q < a.G; ++q) {
-            const float x = __shfl_sync(all, mine, q << gl);
-            rank += (x > mine || (x == mine && q < g)) ? 1 : 0;
-        }
-        const bool speaks = g < a.G && sub == 0;
-        if (scored && a.keep < a.G) {
-            // the last group that stays against the first that does not: errors
-            // of up to two keys and their sum, at most the largest group score's
-            const float big = warp_max(speaks && mine > -INFINITY ? fmaxf(fabsf(b1), fabsf(mine)) : 0.0f);
-            const float in = warp_max(speaks && rank == a.keep - 1 ? mine : -INFINITY);
-            const float out = warp_max(speaks && rank == a.keep ? mine : -INFINITY);
-            if (out > -INFINITY && !(in - out > 4.2f * ks + 7.5e-7f * big)) {
-                rank = group_rank_exact(a, row, top, gkey, b1, b2, ks, sc);
-                if (rank < 0) return false;
-            }
-        }
-        const unsigned kept = __ballot_sync(all, speaks && rank < a.keep);
+        if (fail) return false;
         auto stays = [&](int e) { return (kept >> (((((unsigned)e * a.per_magic) >> 20) << gl) & 31u)) & 1u; };
         if ((a.per & 3) == 0) {                      // four neighbours share their group
 #pragma unroll
@@ -494,10 +548,21 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
         f2 = fmaxf(f2, fminf(f1, v[i]));
         f1 = fmaxf(f1, v[i]);
     }
+    if (W > 1) {                                     // ... of the whole team: the same experts' lanes together
+        team.largest[wid][lane] = make_float2(f1, f2);
+        sync();
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w == wid) continue;
+            const float2 o = team.largest[w][lane];
+            f2 = fmaxf(fmaxf(f2, o.y), fminf(f1, o.x));
+            f1 = fmaxf(f1, o.x);
+        }
+    }
     const uint32_t m1 = sel_on(f1) ? sel_key(f1) : 0u, m2 = sel_on(f2) ? sel_key(f2) : 0u;
     uint32_t lo = max(__reduce_min_sync(all, m1), 1u), hi = __reduce_max_sync(all, m1);
     if (hi == 0) {                                   // nothing eligible: experts 0 .. k-1, weights 0
-        store_weights(a, t, lane, 0.0f, false, 0.0f, 1.0f);
+        if (wid == 0) store_weights(a, t, lane, 0.0f, false, 0.0f, 1.0f);
         return true;
     }
     auto reached = [&](uint32_t x) { return __popc(__ballot_sync(all, m1 >= x)) + __popc(__ballot_sync(all, m2 >= x)); };
@@ -527,13 +592,24 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
         const int u = __shfl_up_sync(all, incl, o);
         if (lane >= o) incl += u;
     }
-    const int C = __shfl_sync(all, incl, 31);
+    int C = __shfl_sync(all, incl, 31), before = 0;
+    if (W > 1) {
+        if (lane == 0) team.count[wid] = C;
+        sync();
+        C = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w == wid) before = C;
+            C += team.count[w];
+        }
+    }
     if (C > kSelCand || C < a.k) return false;
-    for (int p = incl - n; cm; cm &= cm - 1) {
+    for (int p = before + incl - n; cm; cm &= cm - 1) {
         const int i = __ffs(cm) - 1;
         sc.expert[p++] = first(i >> 2) + (i & 3);
     }
-    __syncwarp();
+    sync();
+    if (wid != 0) return true;
     // the last four are filled up with 0, which is behind all
     for (int j = lane; j < ((C + 3) & ~3); j += 32)
         sc.key[j] = j < C ? sel_key(a.bias ? gkey[sc.expert[j]] : sel_cap(__ldg(row + sc.expert[j]))) : 0u;
@@ -560,6 +636,7 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
     return true;
 }
 
+// One token per warp: kSelWarps tokens of a CTA
 template <int CH, bool VEC>
 __global__ void __launch_bounds__(kSelWarps * 32, CH == 8 ? 6 : 8) k_select(const __grid_constant__ SelectArgs a) {
     __shared__ SelScratch scratch[kSelWarps];
@@ -567,18 +644,33 @@ __global__ void __launch_bounds__(kSelWarps * 32, CH == 8 ? 6 : 8) k_select(cons
     const int w = threadIdx.x >> 5;
     const int t = blockIdx.x * kSelWarps + w;
     if (t >= a.T) return;
-    if (!select_fast<CH, VEC>(a, t, scratch[w], gkeys + w * a.key_room)) select_exact<4 * CH>(a, t);
+    SelTeam<1> alone;
+    if (!select_fast<CH, VEC, 1>(a, t, scratch[w], gkeys + w * a.key_room, alone)) select_exact<4 * CH>(a, t);
 }
 
-template <int CH>
+// One token per CTA
+template <int CH, bool VEC>
+__global__ void __launch_bounds__(kSelWarps * 32) k_select_team(const __grid_constant__ SelectArgs a) {
+    __shared__ SelScratch scratch;
+    __shared__ SelTeam<kSelWarps> team;
+    extern __shared__ __align__(16) float gkeys[];   // [key_room] with groups or a bias
+    if (!select_fast<CH, VEC, kSelWarps>(a, blockIdx.x, scratch, gkeys, team) && threadIdx.x < 32) select_exact<32>(a, blockIdx.x);
+}
+
+template <int CH, int TEAM_CH>
 void launch_ch(const SelectArgs& a, cudaStream_t st) {
-    const unsigned grid = (unsigned)((a.T + kSelWarps - 1) / kSelWarps);
-    const size_t smem = a.G > 1 || a.bias ? sizeof(float) * kSelWarps * (size_t)a.key_room : 0;
     // rows of whole, aligned 16-byte vectors
     const bool vec = a.E % 4 == 0 && (a.T == 1 || a.ld % 4 == 0) && (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 &&
                      (reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0;
-    if (vec) k_select<CH, true><<<grid, kSelWarps * 32, smem, st>>>(a);
-    else k_select<CH, false><<<grid, kSelWarps * 32, smem, st>>>(a);
+    const size_t keys = a.G > 1 || a.bias ? sizeof(float) * (size_t)a.key_room : 0;
+    if (a.T <= kSelTeamTokens) {
+        if (vec) k_select_team<TEAM_CH, true><<<a.T, kSelWarps * 32, keys, st>>>(a);
+        else k_select_team<TEAM_CH, false><<<a.T, kSelWarps * 32, keys, st>>>(a);
+        return;
+    }
+    const unsigned grid = (unsigned)((a.T + kSelWarps - 1) / kSelWarps);
+    if (vec) k_select<CH, true><<<grid, kSelWarps * 32, kSelWarps * keys, st>>>(a);
+    else k_select<CH, false><<<grid, kSelWarps * 32, kSelWarps * keys, st>>>(a);
 }
 
 }  // namespace
@@ -589,9 +681,9 @@ cudaError_t launch_select(const SelectArgs& args, cudaStream_t st) {
     while (a.G > 1 && (a.G << (a.group_lanes_log2 + 1)) <= 32) ++a.group_lanes_log2;
     a.per_magic = ((1u << 20) + a.per - 1) / a.per;  // e * magic >> 20 = e / per for e, per <= 1024
     a.key_room = (a.E + 3) & ~3;
-    if (a.E <= 256) launch_ch<2>(a, st);
-    else if (a.E <= 512) launch_ch<4>(a, st);
-    else launch_ch<8>(a, st);
+    if (a.E <= 256) launch_ch<2, 1>(a, st);
+    else if (a.E <= 512) launch_ch<4, 1>(a, st);
+    else launch_ch<8, 2>(a, st);
     return cudaGetLastError();
 }
 

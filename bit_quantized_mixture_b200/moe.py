@@ -111,6 +111,7 @@ def lib():
             "moe_select_experts": [vp, i64, i32, i32, i32, ctypes.POINTER(RoutingRule), vp, vp, vp],
             "moe_set_routing": [vp, ctypes.POINTER(RoutingRule), vp],
             "moe_add_adapters": [vp, i64, vp, i64, vp, i64, i32, i32, vp, ctypes.POINTER(AdapterSet), vp],
+            "moe_adapters_status": [vp],
             "moe_block_norm": [ctypes.POINTER(Norm), vp],
             "moe_block_forward": [vp, ctypes.POINTER(Block), vp],
             "moe_mma_peak_loop": [i32, i32, i64, vp, ctypes.POINTER(ctypes.c_double), vp],
@@ -265,6 +266,12 @@ def add_adapters(x, y, adapter_ids, a, b, scales, ranks=None, out=None, stream=N
         out = _new(tuple(y.shape), y.dtype, _device("y", y), stream)
     binding().add_adapters(x, y, adapter_ids, a, b, scales, ranks, out, _raw(stream))
     return out
+
+
+def adapters_status(stream=None):
+    """Synchronize the stream; raise when an add_adapters call on the current
+    device gave up a bounded wait (moe_adapters_status)."""
+    _check(lib().moe_adapters_status(_stream(stream)))
 
 
 def _gate(gate, T, H, dev):

@@ -347,7 +347,9 @@ moe_status moe_select_experts(const float* logits, int64_t ld_logits, int32_t T,
  * follow `rule` from now on (NULL: softmax + top-k again).  The bias (host or
  * device) is copied on `stream` into the handle; calls on other streams wait
  * for that copy themselves.  With a rule, moe_route_forward runs the router,
- * the selection and moe_forward instead of the one fused kernel.
+ * the selection and moe_forward instead of the one fused kernel.  A captured
+ * graph keeps the rule it was captured with, but reads the handle's bias, which
+ * the next moe_set_routing with a bias overwrites.
  * Errors: as moe_select_experts, for the handle's E and k. */
 moe_status moe_set_routing(moe_handle h, const moe_routing* rule, moe_stream_t stream);
 
@@ -375,6 +377,12 @@ typedef struct {
 moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,
                             int32_t y_fp32, int32_t T, const int32_t* adapter_ids, const moe_adapters* adapters,
                             moe_stream_t stream);
+
+/* Synchronize the stream; MOE_ERR_TIMEOUT when a moe_add_adapters call on the
+ * current device has given up a bounded device-side wait since this was last
+ * asked (its outputs are invalid then; moe_block_forward's adapters report to
+ * moe_sync_status of their handle). */
+moe_status moe_adapters_status(moe_stream_t stream);
 
 #define MOE_GATE_NONE 0
 #define MOE_GATE_CHANNEL 1     /* bf16 [H] */

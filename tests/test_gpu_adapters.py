@@ -54,7 +54,7 @@ SHAPES = [(1, 2048, 2048, 16, 3), (1, 8, 8, 8, 1), (2, 72, 40, 24, 2), (7, 256, 
           (61, 1024, 512, 32, 40), (130, 264, 136, 64, 6), (200, 2048, 256, 16, 11), (333, 136, 72, 56, 2),
           (2113, 136, 72, 24, 7), (2305, 64, 96, 64, 30), (2200, 72, 40, 128, 3), (2049, 520, 264, 96, 4),
           (2801, 136, 72, 24, 7), (2817, 64, 96, 64, 30), (2900, 72, 40, 128, 3), (3000, 520, 264, 96, 4), (2800, 1032, 520, 16, 1), (4001, 128, 64, 8, 2),
-          (8200, 72, 104, 40, 3), (100, 256, 264, 72, 3), (240, 64, 72, 32, 4), (60, 72, 1000, 128, 2)]
+          (8200, 72, 104, 40, 3), (2900, 8, 8, 8, 2), (20000, 64, 72, 16, 5), (100, 256, 264, 72, 3), (240, 64, 72, 32, 4), (60, 72, 1000, 128, 2)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -185,6 +185,20 @@ def test_many_runs_agree():
     for _ in range(40):
         ga, gb = run(a, ida), run(b, idb)
         assert torch.equal(ga, wa) and torch.equal(gb, wb)
+
+
+@pytest.mark.parametrize("T", [200, 1000, 5000])
+def test_two_streams_at_once(T):
+    a, b = make(T, 512, 768, 16, 4, seed=1), make(T, 256, 1024, 64, 3, seed=2, y_dtype=torch.float32)
+    ia, ib = ((torch.arange(T, device=DEV) * q // T - 1).to(torch.int32) for q in (5, 4))
+    run = lambda d, i, **kw: moe.add_adapters(d["x"], d["y"], i, d["a"], d["b"], d["scales"], **kw)
+    wa, wb = run(a, ia), run(b, ib)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [(run(a, ia, stream=s), run(b, ib, stream=t)) for _ in range(10)]
+    torch.cuda.synchronize()
+    moe.adapters_status()
+    assert all(torch.equal(x, wa) and torch.equal(y, wb) for x, y in got)
 
 
 def test_no_tokens():

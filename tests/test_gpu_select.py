@@ -22,10 +22,12 @@ def run(L, k, bias=None, **kw):
 
 
 def check(L, k, bias=None, **kw):
-    ids, w = run(L, k, bias, **kw)
+    """As they are (a CTA per token), and repeated beyond 592 tokens (a warp per token)."""
     rid, rw = O.select_experts(L, k, bias=bias, **kw)
-    assert np.array_equal(ids, rid)
-    assert_weights(L, w, rw, kw.get("scale", 1.0))
+    for n in (1, -(-700 // len(L))):
+        ids, w = run(np.tile(L, (n, 1)), k, bias, **kw)
+        assert np.array_equal(ids, np.tile(rid, (n, 1)))
+        assert_weights(L, w, np.tile(rw, (n, 1)), kw.get("scale", 1.0))
 
 
 def assert_weights(L, w, rw, scale=1.0):
@@ -143,8 +145,9 @@ def test_equal_keys_go_to_the_lowest(biased, groups):
         check(L, k, bias, score=score, num_groups=G, top_groups=keep, group_score=gs)
 
 
-def test_many_tokens_and_row_distance():
-    T, E, k = 3000, 128, 6
+@pytest.mark.parametrize("T", [250, 3000])
+def test_many_tokens_and_row_distance(T):
+    E, k = 128, 6
     rng = np.random.default_rng(2)
     L = rng.standard_normal((T, E)).astype(np.float32)
     bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
@@ -159,8 +162,9 @@ def test_many_tokens_and_row_distance():
     assert_weights(L, w.cpu().numpy()[at], rw)
 
 
-def test_plain_rule_equals_the_built_in_route():
-    T, E, k = 77, 512, 10
+@pytest.mark.parametrize("T", [1, 77, 900])
+def test_plain_rule_equals_the_built_in_route(T):
+    E, k = 512, 10
     layer = moe.MoeLayer(128, 128, E, k, "int4", False, T, 0)
     L = torch.randn(T, E, device=DEV, generator=torch.Generator(DEV).manual_seed(4))
     ids, w = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
@@ -215,9 +219,10 @@ def test_a_layers_routing_rule(T):
     layer.close()
 
 
-def test_streams_and_graphs():
+@pytest.mark.parametrize("T", [50, 800])
+def test_streams_and_graphs(T):
     """On a stream of the caller's, and captured and replayed on new logits."""
-    T, E, k = 50, 512, 10
+    E, k = 512, 10
     rule = moe.Routing("sigmoid", torch.linspace(0, 0.3, E, device=DEV), num_groups=8, top_groups=4, group_score="top2")
     L = torch.randn(T, E, device=DEV)
     want = moe.select_experts(L, k, rule)
