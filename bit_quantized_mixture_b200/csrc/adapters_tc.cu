@@ -169,14 +169,46 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
     const int nk = (a.K + 63) / 64, nn = (a.N + NC - 1) / NC;
     const int k0 = (int)((long long)nk * crank / CL), k1 = (int)((long long)nk * (crank + 1) / CL);
     const int n0 = (int)((long long)nn * crank / CL), n1 = (int)((long long)nn * (crank + 1) / CL);
-    const int early = min(3, k1 - k0);       // (more would keep the adapters' ids waiting behind them)
+    const int early = min(kTcStreams * NBIG, k1 - k0);
     // each tile starts its chunks elsewhere, so that not all CTAs ask for the
     // same lines of A and B at once
     const int turn = t0 / kTcRows * 5 % 4096;
 
-    if (threadIdx.x == 0) {
+    auto rank_of = [&](int id) { return min(a.ranks ? __ldg(a.ranks + id) : a.R, a.R); };
+    // The start: four warps list the tile's adapters while others make the
+    // barriers, send for the first chunks of x (which need no adapter) and take
+    // the tensor memory.
+    if (warp < 4) {
+        // the adapters in order of their first row
+        const int t = t0 + (int)threadIdx.x;
+        const int id = t < a.T ? __ldg(a.ids + t) : -1;
+        const int my_id = id >= 0 && id < a.n && rank_of(id) > 0 ? id : -1;
+        s_id[threadIdx.x] = my_id;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const unsigned same = __match_any_sync(0xffffffffu, my_id);
+        bool leads = my_id >= 0 && lane == __ffs(same) - 1;          // the first row of its adapter
+        for (unsigned todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
+            const int l = __ffs(todo) - 1, lid = __shfl_sync(0xffffffffu, my_id, l);
+            bool seen = false;               // in an earlier warp's rows
+            for (int w = 0; w < warp; ++w) seen = seen || s_id[32 * w + lane] == lid;
+            if (__any_sync(0xffffffffu, seen) && lane == l) leads = false;
+        }
+        const unsigned mine = __ballot_sync(0xffffffffu, leads);
+        if (lane == 0) s_first[warp] = mine;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        int at = __popc(mine & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) at += __popc(s_first[w]);
+        if (leads) {
+            s_list[at] = my_id;
+            s_rank[at] = rank_of(my_id);
+        }
+    } else if (warp == kTcStore && lane == 0) {
         for (int w = 0; w < kTcStreams; ++w) {
-            for (int i = 0; i < NBIG; ++i) { mbar_init(&big_full[w][i], 1); mbar_init(&big_empty[w][i], 1); mbar_init(&chunk_done[w][i], kTcEpiWarps / kTcStreams); }
+            for (int i = 0; i < NBIG; ++i) {
+                mbar_init(&big_full[w][i], 1);
+                mbar_init(&big_empty[w][i], 1);
+                mbar_init(&chunk_done[w][i], kTcEpiWarps / kTcStreams);
+            }
             for (int i = 0; i < NSMALL; ++i) {
                 mbar_init(&small_full[w][i], 1);
                 mbar_init(&small_empty[w][i], 1);
@@ -191,63 +223,27 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
-        // x needs nothing of the adapters: its first chunks are on their way
-        // while their list is made
         Turned kc(k0, k1, turn);
         for (int i = 0; i < early; ++i, kc.next()) {
             const int w = i & (kTcStreams - 1), slot = i / kTcStreams;
             mbar_arrive_expect_tx(&big_full[w][slot], C::BIG);
             tma_load_2d(smem + (w * NBIG + slot) * C::BIG, &maps.x, 64 * kc.at, t0, &big_full[w][slot]);
         }
-    }
-    if (warp == 1) tmem_alloc(&tmem_slot, kTcTmemCols);
-    if (warp == kTcCleaner && lane < 3) {
+    } else if (warp == kTcCleaner) {
+        tmem_alloc(&tmem_slot, kTcTmemCols);
+    } else if (warp == 4 && lane < 3) {
         const CUtensorMap* p = lane == 0 ? &maps.a : (lane == 1 ? &maps.b : &maps.y);
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)p) : "memory");
-    }
-
-    // the tile's adapters in order of their first row, and each row's place among them
-    auto rank_of = [&](int id) { return min(a.ranks ? __ldg(a.ranks + id) : a.R, a.R); };
-    int my_id = -1;
-    if (threadIdx.x < kTcRows) {
-        const int t = t0 + (int)threadIdx.x;
-        const int id = t < a.T ? __ldg(a.ids + t) : -1;
-        if (id >= 0 && id < a.n && rank_of(id) > 0) my_id = id;
-        s_id[threadIdx.x] = my_id;
-    }
-    __syncthreads();
-    cluster_arrive();                        // this CTA's barriers are there for remote arrivals (waited for before the first)
-    bool leads = false;                      // the first row of its adapter
-    if (threadIdx.x < kTcRows) {
-        const unsigned same = __match_any_sync(0xffffffffu, my_id);
-        leads = my_id >= 0 && lane == __ffs(same) - 1;
-        for (unsigned todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
-            const int l = __ffs(todo) - 1, id = __shfl_sync(0xffffffffu, my_id, l);
-            bool seen = false;               // in an earlier warp's rows
-            for (int w = 0; w < warp; ++w) seen = seen || s_id[32 * w + lane] == id;
-            if (__any_sync(0xffffffffu, seen) && lane == l) leads = false;
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, leads);
-        if (lane == 0) s_first[warp] = m;
-    }
-    __syncthreads();
-    int D = 0;
-    {
-        int before = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            if (w == warp) before = D;
-            D += __popc(s_first[w]);
-        }
-        if (leads) {
-            const int at = before + __popc(s_first[warp] & ((1u << lane) - 1u));
-            s_list[at] = my_id;
-            s_rank[at] = rank_of(my_id);
-        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // this CTA's barriers are there for remote arrivals (waited for before the
+    // first; their initialisation was released to the cluster where they were made)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    int D = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) D += __popc(s_first[w]);
     const uint32_t tmem = tmem_slot;
 
     const int passes = max(1, (D + per_pass - 1) / per_pass);      // without an adapter x is let through all the same
@@ -505,7 +501,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                         for (int q = 0; q < CL; ++q) st_cluster_v4(d, q, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
-                asm volatile("fence.proxy.async;" ::: "memory");
+                asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
                 __syncwarp();
                 if (lane < CL) mbar_arrive_cluster(&op_full, lane);
             }
@@ -560,7 +556,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, kTcTmemCols);
+    if (warp == kTcCleaner) tmem_dealloc(tmem, kTcTmemCols);
     if (warp <= kTcStreams || warp >= kTcSmall) cluster_wait();     // of the first arrival
     cluster_arrive();                        // nobody leaves while others may write to its shared memory
     cluster_wait();
