@@ -286,6 +286,12 @@ MOE_DEV void rank_fast(int C, SelScratch& sc) {
     }
 }
 
+// Twice the relative error of a score s (or exp(l - top)) taken by __expf, which is
+// off by 2 + 1.173 |x| ulp with |x| at most 1 - ln s; below kSelTiny nothing is
+// said of it (scores underflow).
+constexpr float kSelTiny = 1e-30f;
+MOE_DEV float score_error(float s) { return 3e-6f + 6e-7f * fabsf(__logf(fmaxf(s, 1e-38f))); }
+
 // The rank of the lane's group (lanes as in select_fast) by fp64 scores; -1:
 // too many members to list.  Only members whose fp32 key reaches their group's
 // second largest (largest: max scores), less both errors, can be among its two
@@ -299,7 +305,7 @@ __device__ __noinline__ int group_rank_exact(const SelectArgs& a, const float* r
     const double total = softmax_total(a, row, top);
     const bool top2 = a.top2 && a.per > 1;
     const float last = top2 && b2 > -INFINITY ? b2 : b1;
-    const float bar = last - (2.1f * ks + 3e-7f * fabsf(last));
+    const float bar = a.bias ? last - (2.1f * ks + 3e-7f * fabsf(last)) : (last > kSelTiny ? last * (1.0f - score_error(last)) : 0.0f);
     int n = 0;
     for (int j0 = 0; j0 < a.per; j0 += L) {
         const int j = j0 + (lane & (L - 1)), e = g * a.per + j;
@@ -390,7 +396,9 @@ MOE_DEV unsigned choose_groups(const SelectArgs& a, const float* row, float top,
         const float big = warp_max(speaks && mine > -INFINITY ? fmaxf(fabsf(b1), fabsf(mine)) : 0.0f);
         const float in = warp_max(speaks && rank == a.keep - 1 ? mine : -INFINITY);
         const float out = warp_max(speaks && rank == a.keep ? mine : -INFINITY);
-        if (out > -INFINITY && !(in - out > 4.2f * ks + 7.5e-7f * big)) {
+        // (without a bias both are sums of scores, whose errors are relative)
+        const float near = a.bias ? 4.2f * ks + 7.5e-7f * big : (in > kSelTiny ? score_error(out) * (in + out) : INFINITY);
+        if (out > -INFINITY && !(in - out > near)) {
             rank = group_rank_exact(a, row, top, gkey, b1, b2, ks, sc);
             fail = rank < 0;
         }
@@ -407,7 +415,9 @@ MOE_DEV unsigned choose_groups(const SelectArgs& a, const float* row, float top,
 //
 // Error bounds.  ks: of a score.  sigmoid: __expf is off by 2 + 1.173 |x| ulp,
 // which the score sees as at most (4 + 0.37 x 2.4) x 2^-24 absolute, plus 3 ulp
-// of the addition and the division: 1e-6 is over twice that.  softmax: __expf
+// of the addition and the division: 1e-6 is over twice that; where the largest
+// logit m of the row is negative the same holds relative to exp(m), with 2 + 1.173 |m|
+// ulp.  softmax: __expf
 // (as above, and x - top rounded) 5 x 2^-24 of the largest score 1/S, the
 // sum S 32 terms in a row, 5 folds and its terms' own errors (the mean of
 // top - x under the softmax is at most ln 1024): 4e-6 / S; 5e-6 / S is taken.
@@ -481,6 +491,17 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
         }
         // without a bias the groups compare exp(l - top) itself, total times the scores
         ks = a.bias ? __fdividef(5e-6f, total) : 5e-6f;
+    }
+    if (a.sigmoid && a.bias) {
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) top = fmaxf(top, v[i]);
+        top = warp_max(top);
+        if (W > 1) {
+            if (lane == 0) team.top[wid] = top;
+            sync();
+            for (int w = 0; w < W; ++w) top = fmaxf(top, team.top[w]);
+        }
+        if (top < 0.0f) ks = __expf(top) * (1e-6f + 3e-7f * fabsf(top)) + 1e-37f;
     }
     if (scored || a.G > 1) {
         const float inv = a.bias ? __fdividef(1.0f, total) : 1.0f;

@@ -116,6 +116,24 @@ def test_extreme_logits(score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shift,spread", [(-30.0, 1.0), (-12.0, 0.01), (0.0, 12.0), (-90.0, 5.0), (20.0, 2.0)])
+@pytest.mark.parametrize("bias", [None, 0.0, 1e-6])
+def test_small_peaked_and_saturated_scores(score, shift, spread, bias):
+    """Scores far below one, one expert that has nearly all, scores near one; biases
+    of the scores' own size."""
+    E, k = 256, 8
+    rng = np.random.default_rng(21)
+    L = (shift + spread * rng.standard_normal((12, E))).astype(np.float32)
+    b = None if bias is None else (bias * rng.standard_normal(E)).astype(np.float32)
+    for G, keep, gs in ((1, 1, "max"), (8, 3, "top2"), (8, 3, "max")):
+        if shift == 20.0 and score == "sigmoid" and (b is not None or gs == "top2"):
+            continue              # 1 - exp(-20): keys and sums differ below 64 bits' own rounding
+        if shift == -90.0 and b is not None:
+            continue              # scores vanish beside any bias
+        check(L, k, b, score=score, num_groups=G, top_groups=keep, group_score=gs)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [(1, 1, "max"), (8, 3, "top2"), (8, 3, "max")])
 def test_keys_nearer_than_fp32_tells(score, groups):
     """Biases that bring every key to one value up to their own rounding
