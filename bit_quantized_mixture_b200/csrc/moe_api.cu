@@ -920,8 +920,24 @@ static bool rows_overlap(const void* p, int64_t lp, int64_t wp, const void* q, i
     return d < wp || d + wq > lp;
 }
 
+// Tokens of a call without a handle: row and tile numbers stay below 2^31
+constexpr int32_t kMaxRows = 1 << 30;
+
+// T rows' distance in bytes (0 for one row, whose ld may be anything)
+static int64_t row_bytes(int64_t ld, int elem_bytes, int32_t T) { return T > 1 ? ld * elem_bytes : 0; }
+
+// a row distance below the rows' width, or so large that their addresses overflow
+static bool bad_distance(int64_t ld, int64_t width, int32_t T, int elem_bytes) {
+    return T > 1 && (ld < width || ld > ((int64_t)1 << 56) / T / elem_bytes);
+}
 static bool bad_rows(const void* p, int64_t ld, int64_t width, int32_t T, int elem_bytes) {
-    return !aligned16(p) || (T > 1 && (ld < width || (ld * elem_bytes) % 16 != 0 || ld > (int64_t)1 << 40));
+    return !aligned16(p) || bad_distance(ld, width, T, elem_bytes) || row_bytes(ld, elem_bytes, T) % 16 != 0;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool spans_meet(const void* p, int64_t np, const void* q, int64_t nq) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
 }
 
 static moe_status check_rule(moe_layer* h, const char* fn, const moe_routing* r, int32_t E, int32_t k) {
@@ -949,8 +965,15 @@ moe_status moe_select_experts(const float* logits, int64_t ld_logits, int32_t T,
     if (T < 0) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: negative T");
     if (T == 0) return MOE_OK;
     if (!logits || !topk_ids || !topk_w) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: null pointer");
-    if (T > 1 && (ld_logits < E || ld_logits > (int64_t)1 << 40))
-        return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: ld_logits below E");
+    if (T > kMaxRows) return fail(nullptr, MOE_ERR_UNSUPPORTED, "moe_select_experts: at most 2^30 tokens");
+    if (bad_distance(ld_logits, E, T, 4))
+        return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: ld_logits below E or out of range");
+    if (!aligned4(logits) || !aligned4(topk_ids) || !aligned4(topk_w) || !aligned4(rule->bias))
+        return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: pointers must be 4-byte aligned");
+    const int64_t in = (T - 1) * row_bytes(ld_logits, 4, T) + (int64_t)E * 4, out = (int64_t)T * k * 4;
+    if (spans_meet(topk_ids, out, topk_w, out) || spans_meet(logits, in, topk_ids, out) || spans_meet(logits, in, topk_w, out) ||
+        (rule->bias && (spans_meet(rule->bias, (int64_t)E * 4, topk_ids, out) || spans_meet(rule->bias, (int64_t)E * 4, topk_w, out))))
+        return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_select_experts: an output overlaps another tensor");
     const cudaError_t e = launch_select(select_args(logits, ld_logits, T, E, k, *rule, rule->bias, topk_ids, topk_w),
                                         (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(nullptr, e, "moe_select_experts");
@@ -982,8 +1005,8 @@ static moe_status check_adapters(moe_layer* h, const char* fn, const moe_adapter
     if (ad->R < 8 || ad->R > kAdapterMaxRank || ad->R % 8 || ad->K < 8 || ad->K % 8 || ad->N < 8 || ad->N % 8)
         return fail(h, MOE_ERR_UNSUPPORTED, "%s: R, K and N must be positive multiples of 8, R at most %d", fn,
                     kAdapterMaxRank);
-    if (!aligned16(ad->a) || !aligned16(ad->b))
-        return fail(h, MOE_ERR_INVALID_ARG, "%s: a and b must be 16-byte aligned", fn);
+    if (!aligned16(ad->a) || !aligned16(ad->b) || !aligned4(ad->scales) || !aligned4(ad->ranks))
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: a and b must be 16-byte aligned, scales and ranks 4-byte aligned", fn);
     return MOE_OK;
 }
 
@@ -1008,12 +1031,15 @@ moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t 
     if (T < 0) return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: negative T", fn);
     if (T == 0) return MOE_OK;
     if (!x || !y || !out || !adapter_ids) return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (T > kMaxRows) return fail(nullptr, MOE_ERR_UNSUPPORTED, "%s: at most 2^30 tokens", fn);
+    if (!aligned4(adapter_ids)) return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: adapter_ids must be 4-byte aligned", fn);
     const int es = y_fp32 ? 4 : 2;
     if (bad_rows(x, ld_x, ad->K, T, 2) || bad_rows(y, ld_y, ad->N, T, es) || bad_rows(out, ld_out, ad->N, T, es))
         return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and at least their width apart", fn);
     const bool in_place = out == y && (ld_out == ld_y || T == 1);
-    if (rows_overlap(x, ld_x * 2, (int64_t)ad->K * 2, out, ld_out * es, (int64_t)ad->N * es, T) ||
-        (!in_place && rows_overlap(y, ld_y * es, (int64_t)ad->N * es, out, ld_out * es, (int64_t)ad->N * es, T)))
+    const int64_t wx = (int64_t)ad->K * 2, wy = (int64_t)ad->N * es, lo = row_bytes(ld_out, es, T);
+    if (rows_overlap(x, row_bytes(ld_x, 2, T), wx, out, lo, wy, T) ||
+        (!in_place && rows_overlap(y, row_bytes(ld_y, es, T), wy, out, lo, wy, T)))
         return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
     const cudaError_t e = launch_add_adapters(adapter_args(x, ld_x, y, ld_y, out, ld_out, y_fp32, T, adapter_ids, ad),
                                               (cudaStream_t)stream);
@@ -1038,6 +1064,7 @@ static moe_status check_norm(moe_layer* h, const char* fn, const moe_norm* n) {
     if (n->T == 0) return MOE_OK;
     if (!n->r || (!n->r_out && !n->x_out) || (!n->x_out) != (!n->w_pre))
         return fail(h, MOE_ERR_INVALID_ARG, "%s: need r, an output, and w_pre exactly with x_out", fn);
+    if (n->T > kMaxRows) return fail(h, MOE_ERR_UNSUPPORTED, "%s: at most 2^30 tokens", fn);
     if (n->gate_kind < MOE_GATE_NONE || n->gate_kind > MOE_GATE_ELEMENT)
         return fail(h, MOE_ERR_INVALID_ARG, "%s: unknown gate kind %d", fn, n->gate_kind);
     if ((n->gate_kind != MOE_GATE_NONE) != (n->gate != nullptr))
@@ -1050,12 +1077,15 @@ static moe_status check_norm(moe_layer* h, const char* fn, const moe_norm* n) {
         (n->r_out && bad_rows(n->r_out, n->ld_r_out, n->H, n->T, es)) ||
         (n->x_out && bad_rows(n->x_out, n->ld_x, n->H, n->T, 2)) ||
         (n->gate_kind == MOE_GATE_ELEMENT && bad_rows(n->gate, n->ld_gate, n->H, n->T, 2)) ||
-        !aligned16(n->w_post) || !aligned16(n->w_pre) || (n->gate_kind == MOE_GATE_CHANNEL && !aligned16(n->gate)))
+        !aligned16(n->w_post) || !aligned16(n->w_pre) || (n->gate_kind == MOE_GATE_CHANNEL && !aligned16(n->gate)) ||
+        (n->gate_kind == MOE_GATE_TOKEN && !aligned4(n->gate)))
         return fail(h, MOE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and at least H apart", fn);
-    const int64_t T = n->T, w2 = (int64_t)n->H * 2, wr = (int64_t)n->H * es;
+    const int32_t T = n->T;
+    const int64_t w2 = (int64_t)n->H * 2, wr = (int64_t)n->H * es;
     struct Rows { const void* p; int64_t ld, w; };
-    const Rows r{n->r, n->ld_r * es, wr}, y{n->y, n->ld_y * 2, w2}, ro{n->r_out, n->ld_r_out * es, wr},
-        xo{n->x_out, n->ld_x * 2, w2}, g{n->gate_kind == MOE_GATE_ELEMENT ? n->gate : nullptr, n->ld_gate * 2, w2};
+    const Rows r{n->r, row_bytes(n->ld_r, es, T), wr}, y{n->y, row_bytes(n->ld_y, 2, T), w2},
+        ro{n->r_out, row_bytes(n->ld_r_out, es, T), wr}, xo{n->x_out, row_bytes(n->ld_x, 2, T), w2},
+        g{n->gate_kind == MOE_GATE_ELEMENT ? n->gate : nullptr, row_bytes(n->ld_gate, 2, T), w2};
     auto clash = [&](const Rows& a, const Rows& b) {
         return a.p && b.p && rows_overlap(a.p, a.ld, a.w, b.p, b.ld, b.w, T);
     };

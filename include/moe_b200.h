@@ -302,9 +302,10 @@ moe_status moe_set_expert_table(moe_handle h, const void* const* blocks, moe_str
  * The pages' checkpoints need none of them; other sparse models with the same
  * experts do.  All are forward operators (the layer serves frozen weights).
  * The calls without a handle run on the current device, which the pointers
- * belong to; T = 0 is a no-op.  Rows are `ld` elements apart (at least the
- * row's width; any value when T <= 1); bf16 and fp32 rows other than logits
- * start on 16-byte boundaries (ld a multiple of 8 for bf16, of 4 for fp32). */
+ * belong to; T = 0 is a no-op, T is at most 2^30.  Rows are `ld` elements
+ * apart (at least the row's width; any value when T <= 1); bf16 and fp32 rows
+ * other than logits start on 16-byte boundaries (ld a multiple of 8 for bf16,
+ * of 4 for fp32), other fp32 and int32 tensors on 4-byte boundaries. */
 
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
@@ -338,8 +339,9 @@ typedef struct {
 } moe_routing;
 
 /* ids int32 [T, k] and weights fp32 [T, k] of fp32 logits [T, E] under
- * `rule` (bias on the device).  1 <= E <= 1024, 1 <= k <= min(E, 32).
- * Errors: INVALID_ARG, UNSUPPORTED (E, k or num_groups), CUDA. */
+ * `rule` (bias on the device).  1 <= E <= 1024, 1 <= k <= min(E, 32); neither
+ * output overlaps the other, the logits or the bias.
+ * Errors: INVALID_ARG, UNSUPPORTED (E, k, num_groups or T), CUDA. */
 moe_status moe_select_experts(const float* logits, int64_t ld_logits, int32_t T, int32_t E, int32_t k,
                               const moe_routing* rule, int32_t* topk_ids, float* topk_w, moe_stream_t stream);
 
@@ -373,7 +375,7 @@ typedef struct {
  * tokens the second product's operand, scale * a x, is held in bf16 for bf16
  * outputs and in three bf16 parts (24 significant bits) for fp32 outputs.
  * Deterministic; needs no workspace.
- * Errors: INVALID_ARG, UNSUPPORTED (R, K or N), CUDA. */
+ * Errors: INVALID_ARG, UNSUPPORTED (R, K, N or T), CUDA. */
 moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,
                             int32_t y_fp32, int32_t T, const int32_t* adapter_ids, const moe_adapters* adapters,
                             moe_stream_t stream);
@@ -413,7 +415,7 @@ typedef struct {
 
 /* Errors: INVALID_ARG (null or misaligned pointers, strides, no output, an
  * output that overlaps another tensor of the call otherwise than allowed),
- * UNSUPPORTED (H), CUDA. */
+ * UNSUPPORTED (H or T), CUDA. */
 moe_status moe_block_norm(const moe_norm* norm, moe_stream_t stream);
 
 /* One MoE block of a model around the handle's layer, the calls above in

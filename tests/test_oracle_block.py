@@ -181,6 +181,44 @@ def test_norm_refusals(kw, status, text):
     assert st == status and text in _err()
 
 
+def test_addresses_and_sizes_out_of_range():
+    """Row distances whose addresses would pass 64 bits, tokens past 2^30, misaligned 4-byte tensors, and
+    selections written over what they read."""
+    L = moe.lib()
+    far = BASE + 32768
+
+    def select(logits=BASE, ld=64, T=4, ids=far, w=far + 4096, bias=None):
+        return L.moe_select_experts(logits, ld, T, 64, 8, _rule(bias=bias), ids, w, None)
+
+    def adapters(T=4, ld=64, ids=BASE, **kw):
+        return L.moe_add_adapters(BASE, ld, BASE + 8192, 64, BASE + 8192, 64, 0, T, ids, _adapters(**kw), None)
+
+    def norm(**kw):
+        return L.moe_block_norm(_norm(**kw), None)
+
+    for st, status, text in (
+            (lambda: select(ld=1 << 62), 1, "out of range"),
+            (lambda: select(ld=1 << 55), 1, "out of range"),
+            (lambda: select(T=(1 << 30) + 1), 2, "2^30"),
+            (lambda: select(logits=BASE + 2), 1, "4-byte"),
+            (lambda: select(ids=far + 1), 1, "4-byte"),
+            (lambda: select(w=far + 4098), 1, "4-byte"),
+            (lambda: select(bias=BASE + 3), 1, "4-byte"),
+            (lambda: select(ids=BASE + 128), 1, "overlaps"),
+            (lambda: select(w=far + 64), 1, "overlaps"),
+            (lambda: select(w=BASE), 1, "overlaps"),
+            (lambda: select(bias=far), 1, "overlaps"),
+            (lambda: adapters(ld=1 << 60), 1, "width apart"),
+            (lambda: adapters(T=(1 << 30) + 1), 2, "2^30"),
+            (lambda: adapters(ids=BASE + 2), 1, "4-byte"),
+            (lambda: adapters(scales=BASE + 2), 1, "4-byte"),
+            (lambda: adapters(ranks=BASE + 1), 1, "4-byte"),
+            (lambda: norm(ld_y=1 << 60), 1, "apart"),
+            (lambda: norm(T=(1 << 30) + 1), 2, "2^30"),
+            (lambda: norm(gate_kind=2, gate=BASE + 2), 1, "aligned")):
+        assert st() == status and text in _err(), text
+
+
 def test_handle_calls_refuse_null():
     L = moe.lib()
     assert L.moe_set_routing(None, _rule(), None) == 1
