@@ -920,7 +920,7 @@ static bool rows_overlap(const void* p, int64_t lp, int64_t wp, const void* q, i
     return d < wp || d + wq > lp;
 }
 
-// Tokens of a call without a handle: row and tile numbers stay below 2^31
+// Tokens of a call without a handle, and columns: row, tile and column numbers stay below 2^31
 constexpr int32_t kMaxRows = 1 << 30;
 
 // T rows' distance in bytes (0 for one row, whose ld may be anything)
@@ -1002,8 +1002,9 @@ moe_status moe_set_routing(moe_handle h, const moe_routing* rule, moe_stream_t s
 static moe_status check_adapters(moe_layer* h, const char* fn, const moe_adapters* ad) {
     if (!ad || !ad->a || !ad->b || !ad->scales) return fail(h, MOE_ERR_INVALID_ARG, "%s: null adapters", fn);
     if (ad->num_adapters < 1) return fail(h, MOE_ERR_INVALID_ARG, "%s: num_adapters must be positive", fn);
-    if (ad->R < 8 || ad->R > kAdapterMaxRank || ad->R % 8 || ad->K < 8 || ad->K % 8 || ad->N < 8 || ad->N % 8)
-        return fail(h, MOE_ERR_UNSUPPORTED, "%s: R, K and N must be positive multiples of 8, R at most %d", fn,
+    if (ad->R < 8 || ad->R > kAdapterMaxRank || ad->R % 8 || ad->K < 8 || ad->K % 8 || ad->N < 8 || ad->N % 8 ||
+        ad->K > kMaxRows || ad->N > kMaxRows)
+        return fail(h, MOE_ERR_UNSUPPORTED, "%s: R, K and N must be positive multiples of 8, R at most %d, K and N 2^30", fn,
                     kAdapterMaxRank);
     if (!aligned16(ad->a) || !aligned16(ad->b) || !aligned4(ad->scales) || !aligned4(ad->ranks))
         return fail(h, MOE_ERR_INVALID_ARG, "%s: a and b must be 16-byte aligned, scales and ranks 4-byte aligned", fn);

@@ -364,7 +364,7 @@ typedef struct {
                                   others are not used, whatever they hold), or NULL: all R */
     int32_t num_adapters;      /* n >= 1 */
     int32_t R;                 /* multiple of 8, 8 .. 128 */
-    int32_t K, N;              /* multiples of 8 */
+    int32_t K, N;              /* multiples of 8, at most 2^30 */
 } moe_adapters;
 
 /* out_t = y_t + scales[i] * b_i (a_i x_t) with i = adapter_ids[t]; a token

@@ -210,6 +210,8 @@ def test_addresses_and_sizes_out_of_range():
             (lambda: select(bias=far), 1, "overlaps"),
             (lambda: adapters(ld=1 << 60), 1, "width apart"),
             (lambda: adapters(T=(1 << 30) + 1), 2, "2^30"),
+            (lambda: adapters(K=(1 << 30) + 8), 2, "2^30"),
+            (lambda: adapters(N=(1 << 30) + 8), 2, "2^30"),
             (lambda: adapters(ids=BASE + 2), 1, "4-byte"),
             (lambda: adapters(scales=BASE + 2), 1, "4-byte"),
             (lambda: adapters(ranks=BASE + 1), 1, "4-byte"),
