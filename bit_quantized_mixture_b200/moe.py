@@ -222,11 +222,17 @@ class Routing:
             _refuse(f"Routing: score must be one of {list(SCORE)}, group_score one of {list(GROUP_SCORE)}")
         if bias is not None and bias.dim() != 1:
             _refuse("Routing: bias must be [E]")
-        self.bias = bias
+        self._bias = bias
         self.E = None if bias is None else bias.shape[0]
         self.c = RoutingRule(SCORE[score], num_groups, top_groups, GROUP_SCORE[group_score], int(bool(renorm)), scale,
                              _cuda("bias", bias, torch.float32, (self.E,), None) if bias is not None else None)
         self.address = ctypes.addressof(self.c)
+
+    @property
+    def bias(self):
+        """The bias that the rule was made with (its address is in the rule: a
+        new bias needs a new Routing, or is copied into this tensor)."""
+        return self._bias
 
 
 def _device(name, t):

@@ -221,6 +221,13 @@ def test_addresses_and_sizes_out_of_range():
         assert st() == status and text in _err(), text
 
 
+def test_a_rules_bias_is_fixed():
+    rule = moe.Routing()
+    assert rule.bias is None
+    with pytest.raises(AttributeError):
+        rule.bias = torch.zeros(4)
+
+
 def test_handle_calls_refuse_null():
     L = moe.lib()
     assert L.moe_set_routing(None, _rule(), None) == 1
