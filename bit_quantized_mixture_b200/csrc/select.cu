@@ -20,8 +20,8 @@
 // nothing is rounded.
 //
 // What bounds it: instructions.  32768 tokens of 1024 experts (k = 32) issue about
-// 1200 per token and warp, 0.63 per cycle and scheduler, in 51 us, where the
-// logits alone stream in 21 us; of 8192 tokens of 512 experts in 8 groups (18 us)
+// 1200 per token and warp, 0.63 per cycle and scheduler, in 50 us, where the
+// logits alone stream in 21 us; of 8192 tokens of 512 experts in 8 groups (17 us)
 // a quarter goes to the scores, a quarter to the groups.  Warps that walk through
 // several tokens and load the next row while they rank one were slower (64 and
 // 22 us: a fixed share of tokens per warp against the hardware's own hand-out).
@@ -44,6 +44,20 @@ constexpr int kSelTeamTokens = 592;
 constexpr int kSelCand = 64;         // candidates that a warp's list holds
 constexpr int kSelSpare = 4;         // ... and may hold beyond k of the lanes' largest keys
 
+// the largest of a warp's values (redux.sync on fp32: one instruction in place of
+// five shuffles and five maxima)
+MOE_DEV float warp_max1(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+// exp by the approximate power of two, with __expf's error; results below 2^-126 are
+// 0 (__expf keeps them, for three more instructions): within the bounds below
+MOE_DEV float exp_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+    return r;
+}
 MOE_DEV double warp_sum_d(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -70,11 +84,14 @@ MOE_DEV void store_weights(const SelectArgs& a, int t, int id, float x, bool on,
     const bool live = lane < a.k && on;
     float w = 0.0f;
     if (a.renorm) {
-        const float mx = warp_max(live ? x : -INFINITY);
+        const float mx = warp_max1(live ? x : -INFINITY);
         if (live) {
-            if (!a.sigmoid) w = expf(x - mx);
-            else if (x > 0.0f) w = __fdiv_rn(1.0f, 1.0f + expf(-x));
-            else w = __fdiv_rn(expf(x - fminf(mx, 0.0f)), 1.0f + expf(x));
+            if (!a.sigmoid) {
+                w = expf(x - mx);
+            } else {
+                const float e = expf(-fabsf(x));
+                w = __fdiv_rn(x > 0.0f ? 1.0f : (mx < 0.0f ? expf(x - mx) : e), 1.0f + e);
+            }
         }
         const float sum = warp_sum(w);
         w = live ? __fdiv_rn(w, sum) : 0.0f;
@@ -135,7 +152,7 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
         }
     }
     any = __any_sync(0xffffffffu, any);
-    top = warp_max(top);
+    top = warp_max1(top);
     double total = 0.0;
     if (!a.sigmoid && any) {
 #pragma unroll 1
@@ -296,7 +313,7 @@ MOE_DEV void rank_fast(int C, SelScratch& sc) {
     }
 }
 
-// Twice the relative error of a score s (or exp(l - top)) taken by __expf, which is
+// Twice the relative error of a score s (or exp(l - top)) taken by exp_approx, which is
 // off by 2 + 1.173 |x| ulp with |x| at most 1 - ln s; below kSelTiny nothing is
 // said of it (scores underflow).
 constexpr float kSelTiny = 1e-30f;
@@ -403,9 +420,9 @@ MOE_DEV unsigned choose_groups(const SelectArgs& a, const float* row, float top,
     if (scored && a.keep < a.G) {
         // the last group that stays against the first that does not: errors
         // of up to two keys and their sum, at most the largest group score's
-        const float big = warp_max(speaks && mine > -INFINITY ? fmaxf(fabsf(b1), fabsf(mine)) : 0.0f);
-        const float in = warp_max(speaks && rank == a.keep - 1 ? mine : -INFINITY);
-        const float out = warp_max(speaks && rank == a.keep ? mine : -INFINITY);
+        const float big = warp_max1(speaks && mine > -INFINITY ? fmaxf(fabsf(b1), fabsf(mine)) : 0.0f);
+        const float in = warp_max1(speaks && rank == a.keep - 1 ? mine : -INFINITY);
+        const float out = warp_max1(speaks && rank == a.keep ? mine : -INFINITY);
         // (without a bias both are sums of scores, whose errors are relative)
         const float near = a.bias ? 4.2f * ks + 7.5e-7f * big : (in > kSelTiny ? score_error(out) * (in + out) : INFINITY);
         if (out > -INFINITY && !(in - out > near)) {
@@ -423,11 +440,11 @@ MOE_DEV unsigned choose_groups(const SelectArgs& a, const float* row, float top,
 // than their errors are taken again in fp64.  false: the candidates are more
 // than the list holds, or fewer than k; nothing is written.
 //
-// Error bounds.  ks: of a score.  sigmoid: __expf is off by 2 + 1.173 |x| ulp,
+// Error bounds.  ks: of a score.  sigmoid: exp_approx is off by 2 + 1.173 |x| ulp,
 // which the score sees as at most (4 + 0.37 x 2.4) x 2^-24 absolute, plus 3 ulp
 // of the addition and the division: 1e-6 is over twice that; where the largest
 // logit m of the row is negative the same holds relative to exp(m), with 2 + 1.173 |m|
-// ulp.  softmax: __expf
+// ulp.  softmax: exp_approx
 // (as above, and x - top rounded) 5 x 2^-24 of the largest score 1/S, the
 // sum S 32 terms in a row, 5 folds and its terms' own errors (the mean of
 // top - x under the softmax is at most ln 1024): 4e-6 / S; 5e-6 / S is taken.
@@ -484,14 +501,14 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
         }
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) top = fmaxf(top, v[i]);
-        top = warp_max(top);
+        top = warp_max1(top);
         if (W > 1) {
             if (lane == 0) team.top[wid] = top;
             sync();
             for (int w = 0; w < W; ++w) top = fmaxf(top, team.top[w]);
         }
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) s += __expf(v[i] - top);     // 0 for those that are off
+        for (int i = 0; i < SLOTS; ++i) s += exp_approx(v[i] - top);     // 0 for those that are off
         total = warp_sum(s);
         if (W > 1) {
             if (lane == 0) team.sum[wid] = total;
@@ -505,7 +522,7 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
     if (a.sigmoid && a.bias) {
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) top = fmaxf(top, v[i]);
-        top = warp_max(top);
+        top = warp_max1(top);
         if (W > 1) {
             if (lane == 0) team.top[wid] = top;
             sync();
@@ -525,10 +542,10 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
             if (scored) {
                 if (a.sigmoid) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) g[q] = rcp_approx(1.0f + __expf(-g[q]));
+                    for (int q = 0; q < 4; ++q) g[q] = rcp_approx(1.0f + exp_approx(-g[q]));
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) g[q] = __expf(g[q] - top) * inv;
+                    for (int q = 0; q < 4; ++q) g[q] = exp_approx(g[q] - top) * inv;
                 }
             }
 #pragma unroll
