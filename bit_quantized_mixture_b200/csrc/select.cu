@@ -670,9 +670,11 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
             const int j1 = sc.order[lane], j2 = sc.order[lane + 1];
             const float x = sel_value(sc.key[j1]), y = sel_value(sc.key[j2]);
             if (!(x - y > 2.0f * ks + 2.4e-7f * fmaxf(fabsf(x), fabsf(y)))) {
-                // equal logits and biases are equal keys: the lower expert first
+                // equal logits and biases are equal keys: the lower expert first.  Behind
+                // the k-th an equal key says nothing: the one after it may be nearer
+                // than fp32 tells, and is not looked at.
                 const int e1 = sc.expert[j1], e2 = sc.expert[j2];
-                near = !(sel_cap(__ldg(row + e1)) == sel_cap(__ldg(row + e2)) && sel_cap(__ldg(a.bias + e1)) == sel_cap(__ldg(a.bias + e2)));
+                near = !(lane + 1 < a.k && sel_cap(__ldg(row + e1)) == sel_cap(__ldg(row + e2)) && sel_cap(__ldg(a.bias + e1)) == sel_cap(__ldg(a.bias + e2)));
             }
         }
         if (__any_sync(all, near)) rank_exact(a, row, top, C, sc);

@@ -150,6 +150,24 @@ def test_keys_nearer_than_fp32_tells(score, groups):
     check(L, k, bias, score=score, num_groups=G, top_groups=keep, group_score=gs)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 2, 5])
+@pytest.mark.parametrize("equal", [2, 3, 30])
+def test_equal_keys_at_the_border_hide_no_larger_one(score, k, equal):
+    """`equal` experts with one logit and bias, and behind them one whose key is larger by less than fp32
+    tells (a saturated sigmoid, or a bias that absorbs the difference): it comes first."""
+    E, T = 64, 4
+    L = np.full((T, E), -40.0, dtype=np.float32)
+    bias = np.zeros(E, dtype=np.float32)
+    L[:, 3:3 + equal] = 21.5
+    L[:, 50] = 30.0 if score == "sigmoid" else 21.501
+    if score == "softmax":
+        bias[:] = 1e5
+    want, _ = O.select_experts(L, k, score=score, bias=bias)
+    assert (want[:, 0] == 50).all()
+    check(L, k, bias, score=score)
+
+
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("groups", [(1, 1, "max"), (4, 2, "top2"), (8, 4, "max")])
 def test_equal_keys_go_to_the_lowest(biased, groups):
