@@ -410,10 +410,21 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                     const int rank = s_rank[d], steps = (rank + 15) / 16;
                     if (rank & 15) {
                         uint8_t* bt = smem + C::OFF_SMALL + (w * NSMALL + slot) * C::SMALL;
-                        for (int i = lane; i < NC * 16; i += 32) {
-                            const int r = i >> 4, col = 16 * (steps - 1) + (i & 15);
-                            if (col >= rank)
-                                *reinterpret_cast<uint16_t*>(bt + (col >> 6) * NC * 128 + sw_piece(r, (col & 63) >> 3) + 2 * (col & 7)) = 0;
+                        // a row of the step is two pieces of eight columns: the one
+                        // that the rank ends in keeps `left` of them, one behind it none
+                        const int col = rank & ~7, left = rank & 7, end = 16 * steps;
+                        uint32_t keep[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) keep[q] = (left > 2 * q ? 0xffffu : 0u) | (left > 2 * q + 1 ? 0xffff0000u : 0u);
+                        uint8_t* block = bt + (col >> 6) * NC * 128;
+#pragma unroll
+                        for (int r = lane; r < NC; r += 32) {
+                            uint4* piece = reinterpret_cast<uint4*>(block + sw_piece(r, (col & 63) >> 3));
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (left) v = *piece;
+                            *piece = make_uint4(v.x & keep[0], v.y & keep[1], v.z & keep[2], v.w & keep[3]);
+                            if (end - col > 8)
+                                *reinterpret_cast<uint4*>(block + sw_piece(r, ((col & 63) >> 3) + 1)) = make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
                     }
