@@ -26,7 +26,7 @@
 //
 // Warps: 0 loads x and y, 11-12 A and B (TMA; one thread for all of it spends longer on
 // its waits and loads than a chunk takes), 1-2 MMA issuers, 3-10 epilogue (two groups
-// of a thread per row), 13 cleans B's unused columns, 14 stores.
+// of a thread per row), 13 and 15 clean B's unused columns, 14 stores.
 // Bound by memory: x and y in, out once; the adapters come from L2.
 #include <cooperative_groups.h>
 #include <cuda.h>
@@ -44,8 +44,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kTcRows = 128;
 constexpr int kTcEpiWarps = 8;           // 4 per stream
-constexpr int kTcSmall = 11, kTcCleaner = 13, kTcStore = 14;     // warps
-constexpr int kTcThreads = 32 * (kTcStore + 1);
+constexpr int kTcSmall = 11, kTcCleaner = 13, kTcStore = 14, kTcCleaner1 = 15;     // warps
+constexpr int kTcThreads = 32 * (kTcCleaner1 + 1);
 // Two of everything per chunk: an MMA issuer waits, issues and commits for about
 // 700 cycles per chunk of x, and the epilogue of an output chunk is a chain of
 // about 1270, where a chunk's way from memory takes 700 and 1400.  So two issuers
@@ -393,20 +393,19 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             bulk_wait_all();
         }
         __syncwarp();
-    } else if (warp == kTcCleaner) {
+    } else if (warp == kTcCleaner || warp == kTcCleaner1) {
         // With ranks of their own, adapters' B columns behind the rank may hold
         // anything: those of the last k step are zeroed where they arrived.
         if (a.ranks) {
             // the first product's uses of the slots are over then, and the slots
             // go on where it left off
             bool ok = D == 0 || __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 57));
-            int used[kTcStreams];
-            for (int w = 0; w < kTcStreams; ++w) used[w] = D * count(k0, k1, w);
-            for (int nc = n0; ok && nc < n1; ++nc) {
-                const int w = (nc - n0) & (kTcStreams - 1);
-                for (int d = 0; d < D; ++d, ++used[w]) {
-                    const int slot = used[w] % NSMALL;
-                    if (!(ok = all_wait(&small_full[w][slot], (uint32_t)(used[w] / NSMALL) & 1u, &abort_flag, err, 56))) break;
+            const int w = warp == kTcCleaner ? 0 : 1;
+            int used = D * count(k0, k1, w);
+            for (int nc = n0 + w; ok && nc < n1; nc += kTcStreams) {
+                for (int d = 0; d < D; ++d, ++used) {
+                    const int slot = used % NSMALL;
+                    if (!(ok = all_wait(&small_full[w][slot], (uint32_t)(used / NSMALL) & 1u, &abort_flag, err, 56))) break;
                     const int rank = s_rank[d], steps = (rank + 15) / 16;
                     if (rank & 15) {
                         uint8_t* bt = smem + C::OFF_SMALL + (w * NSMALL + slot) * C::SMALL;
