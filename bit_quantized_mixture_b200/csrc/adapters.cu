@@ -29,11 +29,15 @@ constexpr int kAdTokenMax = 256, kAdTokenWork = 8192;        // most tokens, mos
 // CTAs per token: rank 16, 1 token 3.8 us with 8, 4.6 with 4, 6.9 with 2; 64 tokens
 // 5.6 / 5.4 / 7.1; 128 tokens 9.8 / 6.4 / 7.6; 256 tokens 18 / 11.4 / 9.4.
 constexpr int kAdCluster8 = 32, kAdCluster4 = 192;           // up to so many tokens 8, 4 CTAs
-// Tiles of 16 against 64 tokens: 1024 tokens rank 16 8.7 / 12 us, 4096 tokens 29 / 25;
-// tiles of 128 on tcgen05 (adapters_tc.cu) against those: 2048 tokens rank 16 22 / 15,
-// 4096 tokens 24 / 25, 8192 tokens rank 64 40 / 59; with fp32 outputs (three parts of
-// z) 4096 tokens rank 16 34 / 32, 8192 tokens 52 / 54, rank 64 72 / 81.
-constexpr int kAdSmallTile = 2048, kAdTcMin = 2800, kAdTcMinWide = 8192;
+// 2048 -> 2048, 12 requests in order, us, tiles of 16 tokens / of 128 on tcgen05
+// (adapters_tc.cu), bf16: rank 16, 2000 tokens 14.5 / 21, 2800 tokens 20.3 / 20.3, 8192
+// tokens 53 / 31; rank 64, 2000 tokens 23 / 25, 2300 tokens 26.2 / 25.6, 8192 tokens
+// 75 / 39; rank 128, 1000 tokens 29.6 / 31, 1500 tokens 42 / 34, 8192 tokens 183 / 65.
+// fp32 outputs (three parts of z), tiles of 16 / of 64 / tcgen05: rank 16, 3300 tokens
+// 28 / 31 / 34, 4096 tokens 34 / 32 / 33, 8192 tokens 63 / 52 / 48; rank 64, 3300 tokens
+// 39 / 54 / 43, 8192 tokens 87 / 81 / 71.
+constexpr int kAdTc32 = 2800, kAdTc64 = 2300, kAdTc128 = 1500;   // from so many tokens on tcgen05: ranks to 32, 64, 128
+constexpr int kAdSmallWide = 3600, kAdTcWide = 8192;             // fp32: up to so many in tiles of 16, from so many on tcgen05
 constexpr int kAdThreads = 256;
 
 MOE_DEV float dot8(const uint4& p, const uint4& q, float s) {
@@ -462,11 +466,11 @@ cudaError_t launch_tile(const AdapterArgs& a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, k_adapter_tile<RG, MT, MG, WIDE>, a);
 }
 
-template <int MT, int MG>
+template <int MT, int MG, bool WIDE>
 cudaError_t launch_tiles(const AdapterArgs& a, cudaStream_t st) {
-    if (a.R <= 32) return a.wide ? launch_tile<1, MT, MG, true>(a, st) : launch_tile<1, MT, MG, false>(a, st);
-    if (a.R <= 64) return a.wide ? launch_tile<2, MT, MG, true>(a, st) : launch_tile<2, MT, MG, false>(a, st);
-    return a.wide ? launch_tile<4, MT, MG, true>(a, st) : launch_tile<4, MT, MG, false>(a, st);
+    if (a.R <= 32) return launch_tile<1, MT, MG, WIDE>(a, st);
+    if (a.R <= 64) return launch_tile<2, MT, MG, WIDE>(a, st);
+    return launch_tile<4, MT, MG, WIDE>(a, st);
 }
 
 }  // namespace
@@ -476,11 +480,12 @@ cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st) {
         if (a.T <= kAdCluster8) return launch_tokens<8>(a, st);
         return a.T <= kAdCluster4 ? launch_tokens<4>(a, st) : launch_tokens<2>(a, st);
     }
-    if (a.T >= (a.wide ? kAdTcMinWide : kAdTcMin)) {
+    if (a.T >= (a.wide ? kAdTcWide : a.R <= 32 ? kAdTc32 : a.R <= 64 ? kAdTc64 : kAdTc128)) {
         const cudaError_t e = launch_add_adapters_tc(a, st);
         if (e != cudaErrorNotSupported) return e;
     }
-    return a.T <= kAdSmallTile ? launch_tiles<1, 1>(a, st) : launch_tiles<2, 2>(a, st);
+    if (!a.wide) return launch_tiles<1, 1, false>(a, st);
+    return a.T <= kAdSmallWide ? launch_tiles<1, 1, true>(a, st) : launch_tiles<2, 2, true>(a, st);
 }
 
 }  // namespace moe

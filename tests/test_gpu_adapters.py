@@ -72,6 +72,17 @@ def test_matches_the_oracle(shape, wide, order):
     assert_close(out, d, ids)
 
 
+@pytest.mark.parametrize("T,R,wide", [(1499, 72, False), (1500, 72, False), (2299, 64, False), (2300, 40, False), (2799, 32, False), (2800, 8, False),
+                                      (3600, 16, True), (3601, 16, True), (3700, 64, True), (3605, 128, True), (8192, 72, True)])
+def test_both_sides_of_each_token_count_that_changes_the_kernel(T, R, wide):
+    K, N, n = 136, 72, 5
+    d = make(T, K, N, R, n, seed=T + R, y_dtype=torch.float32 if wide else torch.bfloat16)
+    g = torch.Generator().manual_seed(T)
+    ids = torch.randint(-1, n, (T,), generator=g).sort().values.to(torch.int32).to(DEV)
+    ranks = torch.randint(1, R + 1, (n,), generator=g).to(torch.int32).to(DEV)
+    assert_close(moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"], ranks), d, ids, ranks)
+
+
 @pytest.mark.parametrize("T", [1, 40, 200, 300, 2100, 2900, 8300])
 @pytest.mark.parametrize("wide", [False, True])
 def test_ranks_of_their_own(T, wide):
