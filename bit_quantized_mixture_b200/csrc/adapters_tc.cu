@@ -395,7 +395,10 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         __syncwarp();
     } else if (warp == kTcCleaner || warp == kTcCleaner1) {
         // With ranks of their own, adapters' B columns behind the rank may hold
-        // anything: those of the last k step are zeroed where they arrived.
+        // anything: those of the last k step are zeroed where they arrived, whole
+        // pieces by a warp per stream (rank <= 16, 16 requests, 8192 tokens: column by
+        // column and one warp 61 us, by pieces 41, two warps 37; without ranks of
+        // their own 31).
         if (a.ranks) {
             // the first product's uses of the slots are over then, and the slots
             // go on where it left off
