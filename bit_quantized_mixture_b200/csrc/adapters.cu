@@ -9,7 +9,7 @@
 // per output; the rows of B are on their way meanwhile.
 #include <cooperative_groups.h>
 
-#include "common.cuh"
+#include "adapters.cuh"
 #include "kernels.h"
 
 namespace moe {
@@ -203,6 +203,7 @@ MOE_DEV void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
 // RG: groups of 32 rank rows.  z is held in bf16 (half a step 2^-8 of a term that
 // is then rounded into a bf16 output); WIDE, y and out fp32: in three bf16 parts,
 // 24 significant bits (two left 1.6e-6 of the output, sixteen times fp32's error).
+// Ranks that are not in use have z = 0, whatever x holds.
 constexpr int kTileCluster = 4;
 constexpr int kTileWarps = 8;
 
@@ -212,6 +213,27 @@ constexpr size_t tile_smem_bytes() {
     return (size_t)(kTileWarps / MG) * MG * MT * 4 * RG * 2 * 32 * sizeof(float2);
 }
 
+// Eight outputs of a row whose products hold a NaN, taken again in fp32 (rare: not
+// inlined).  zrow: the row's words of z, part q at q * stride (see zf below).
+template <int RG, bool WIDE>
+__device__ __noinline__ void tile_repair(const AdapterArgs& a, int t, int col, int id, int rank, const uint32_t* zrow, int stride) {
+    auto z_of = [&](int r) {
+        const int j = 4 * (r >> 5) + ((r >> 1) & 3);
+        const uint32_t* w = zrow + (j >> 1) * 128 + ((r >> 3) & 3) * 4 + (j & 1) * 2;
+        float v = 0.0f;
+        for (int q = WIDE ? 2 : 0; q >= 0; --q) v += r & 1 ? bf16_hi(w[q * stride]) : bf16_lo(w[q * stride]);
+        return v;
+    };
+    const bool nan = any_nan(z_of, rank);            // a NaN in z spoils them all
+    const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(a.b) + ((size_t)id * a.N + col) * a.R;
+    for (int u = 0; u < 8; ++u, b += a.R) {
+        const float s = nan ? NAN : whole_product(z_of, b, rank);
+        const size_t yo = (size_t)t * a.ld_y + col + u, oo = (size_t)t * a.ld_out + col + u;
+        if (WIDE) reinterpret_cast<float*>(a.out)[oo] = reinterpret_cast<const float*>(a.y)[yo] + s;
+        else reinterpret_cast<__nv_bfloat16*>(a.out)[oo] = __float2bfloat16_rn(bf16_to_f(reinterpret_cast<const __nv_bfloat16*>(a.y)[yo]) + s);
+    }
+}
+
 template <int RG, int MT, int MG, bool WIDE>
 __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_tile(const __grid_constant__ AdapterArgs a) {
     constexpr int BT = 16 * MT * MG, PARTS = kTileWarps / MG, TJ = 4 * RG, NPASS = RG == 4 ? 2 : 1, PJ = TJ / NPASS;
@@ -219,6 +241,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
     constexpr int ZPARTS = WIDE ? 3 : 1;                  // bf16 parts that z is held in
     extern __shared__ __align__(16) float2 part_s[];      // [PARTS][ZN]; later zf in place of part 1 on
     __shared__ float s_scale[BT];
+    __shared__ int s_rank[BT];                            // 0: no adapter
     cg::cluster_group cl = cg::this_cluster();
     const int crank = (int)cl.block_rank();
     const int t0 = (int)(blockIdx.x / kTileCluster) * BT;
@@ -232,7 +255,11 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
         const int id = __ldg(a.ids + r0 + lane);
         if (id >= 0 && id < a.n && rank_of(id) > 0) myid = id;
     }
-    if (part == 0 && lane < 16 * MT) s_scale[16 * MT * mg + lane] = myid >= 0 ? __ldg(a.scales + myid) : 0.0f;
+    const int myrank = myid >= 0 ? rank_of(myid) : 0;
+    if (part == 0 && lane < 16 * MT) {
+        s_scale[16 * MT * mg + lane] = myid >= 0 ? __ldg(a.scales + myid) : 0.0f;
+        s_rank[16 * MT * mg + lane] = myrank;
+    }
     const unsigned with = __ballot_sync(0xffffffffu, myid >= 0);
     const int share = crank * PARTS + part;
     constexpr int SHARES = kTileCluster * PARTS;
@@ -327,15 +354,13 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
         }
         const int l = i & 31, h = (i >> 5) & 1, j = (i >> 6) % TJ, mm = (i >> 6) / TJ;     // mm: 16-row tile of the block
         const float sc = s_scale[16 * mm + 8 * h + (l >> 2)];
-        v.x *= sc;
-        v.y *= sc;
+        const int left = s_rank[16 * mm + 8 * h + (l >> 2)] - (32 * (j >> 2) + 8 * (l & 3) + 2 * (j & 3));     // ranks in use from this pair on
+        v.x = left > 0 ? v.x * sc : 0.0f;
+        v.y = left > 1 ? v.y * sc : 0.0f;
         const int w = ((mm * 2 * RG + (j >> 1)) * 32 + l) * 4 + (j & 1) * 2 + h;
 #pragma unroll
         for (int q = 0; q < ZPARTS; ++q) {
-            const uint32_t p = pack_bf16x2(v.x, v.y);
-            zf[q * ZN + w] = p;
-            v.x -= bf16_lo(p);
-            v.y -= bf16_hi(p);
+            zf[q * ZN + w] = ZPARTS > 1 ? take_bf16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
         }
     }
     // the others may still read this CTA's sums: waited for at the end
@@ -419,6 +444,16 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
                 if (r0 + g + 8 * u >= a.T || col >= a.N) continue;
                 const int m = u >> 1, h = u & 1;
                 const bool own = (with >> (8 * u + g)) & 1u;          // rows without an adapter keep y's bits
+                bool odd = false;
+                if (own && ZPARTS > 1) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) odd = odd || delta[m][j][2 * h] != delta[m][j][2 * h] || delta[m][j][2 * h + 1] != delta[m][j][2 * h + 1];
+                }
+                if (odd) {
+                    const int t = r0 + g + 8 * u, row = t - t0;
+                    tile_repair<RG, WIDE>(a, t, col, __ldg(a.ids + t), s_rank[row], zf + ((row >> 4) * 2 * RG * 32 + 4 * g) * 4 + h, ZN);
+                    continue;
+                }
                 const size_t off = (size_t)(r0 + g + 8 * u) * a.ld_out + col;
                 uint32_t* y = &yv[u][0].x;
                 if (WIDE) {

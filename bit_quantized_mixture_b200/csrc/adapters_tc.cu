@@ -31,7 +31,7 @@
 #include <cooperative_groups.h>
 #include <cuda.h>
 
-#include "common.cuh"
+#include "adapters.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
 
@@ -143,6 +143,32 @@ MOE_DEV void wait_some(uint64_t* bar, uint32_t parity) {
 
 // where a call without an error word of its own records a wait that gave up
 __device__ int g_wait_err;
+
+// 32 output columns of a row whose products hold a NaN, taken again in fp32 (rare:
+// not inlined): n: the first column's number, c: its place in the chunk at `tile`
+// (which holds y), op: z's parts
+template <int RB, bool WIDE>
+__device__ __noinline__ void tc_repair(const AdapterArgs& a, int id, int rank, int n, int row, uint8_t* tile, int c, const uint8_t* op) {
+    using C = TcCfg<RB, WIDE>;
+    auto z_of = [&](int r) {
+        float v = 0.0f;
+        for (int h = C::PARTS - 1; h >= 0; --h)
+            v += bf16_to_f(*reinterpret_cast<const __nv_bfloat16*>(op + (h * RB + (r >> 6)) * C::ZBLOCK + sw_piece(row, (r & 63) >> 3) + (r & 7) * 2));
+        return v;
+    };
+    const bool nan = any_nan(z_of, rank);            // a NaN in z spoils them all
+    const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(a.b) + ((size_t)id * a.N + n) * a.R;
+    for (int u = 0; u < 32 && n + u < a.N; ++u, b += a.R) {
+        const float s = nan ? NAN : whole_product(z_of, b, rank);
+        if (WIDE) {
+            float* p = reinterpret_cast<float*>(tile + sw_piece(row, (c + u) >> 2)) + ((c + u) & 3);
+            *p += s;
+        } else {
+            __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(tile + sw_piece(row, (c + u) >> 3)) + ((c + u) & 7);
+            *p = __float2bfloat16_rn(bf16_to_f(*p) + s);
+        }
+    }
+}
 
 template <int RB, bool WIDE>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -506,11 +532,8 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                     for (int h = 0; h < C::PARTS; ++h, d += RB * C::ZBLOCK) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            w[q] = pack_bf16x2(z[2 * q], z[2 * q + 1]);
-                            z[2 * q] -= bf16_lo(w[q]);
-                            z[2 * q + 1] -= bf16_hi(w[q]);
-                        }
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = C::PARTS > 1 ? take_bf16x2(z[2 * q], z[2 * q + 1]) : pack_bf16x2(z[2 * q], z[2 * q + 1]);
                         for (int q = 0; q < CL; ++q) st_cluster_v4(d, q, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
@@ -524,7 +547,9 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         // where its stream left off.
         if (D == 0) ok = all_wait(&z_full, 0u, &abort_flag, err, 58);
         int unit = 0, big = passes * count(k0, k1, group);
-        for (int nc = n0 + group; ok && nc < n1; nc += kTcStreams, ++big) {
+        Turned at(n0, n1, turn);
+        if (group) at.next();
+        for (int nc = n0 + group; ok && nc < n1; nc += kTcStreams, ++big, at.next(), at.next()) {
             const int s = big % NBIG;
             if (!(ok = all_wait(&big_full[group][s], (uint32_t)(big / NBIG) & 1u, &abort_flag, err, 54))) break;
             uint8_t* tile = smem + (group * NBIG + s) * C::BIG;
@@ -539,7 +564,11 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                     for (int c = 0; c < NC; c += 32) {
                         uint32_t r[32];
                         tmem_ld_x32c(src + (uint32_t)c, r);
-                        if (mine == d) {
+                        if (mine == d && C::PARTS > 1 && sum_is_nan(r)) {
+                            // (the operand is complete; this thread has not seen it yet)
+                            if (mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 53))
+                                tc_repair<RB, WIDE>(a, id, s_rank[d], NC * at.at + c, row, tile, c, smem + C::OFF_OP);
+                        } else if (mine == d) {
 #pragma unroll
                             for (int j = 0; j < (WIDE ? 8 : 4); ++j) {
                                 uint4* p = reinterpret_cast<uint4*>(tile + sw_piece(row, c / 8 + j));

@@ -1,0 +1,64 @@
+"""moe_add_adapters, the same in each of its kernels: infinities, values at the
+ends of fp32, and how exactly the second product's operand is held."""
+import numpy as np
+import pytest
+import torch
+
+from bit_quantized_mixture_b200 import moe
+from oracle import moe_oracle as O
+from tests.test_gpu_adapters import DEV, f64, make
+
+pytestmark = pytest.mark.gpu
+
+# tokens and rank of each kernel: a cluster per token, tiles of 16, tiles of 64
+# (fp32 outputs), tcgen05 with its ranks up to 64 and up to 128
+SIZES = [(20, 8), (300, 16), (700, 128), (1600, 128), (2900, 16), (3700, 16), (3700, 72), (8300, 64)]
+
+
+def oracle(d, ids, ranks=None):
+    with np.errstate(all="ignore"):
+        return O.add_adapters(*(f64(d[i]) for i in ("x", "y")), ids.cpu().numpy(), *(f64(d[i]) for i in ("a", "b", "scales")),
+                              None if ranks is None else ranks.cpu().numpy())
+
+
+def same_kind(out, want):
+    """Finite where the exact value is, the same infinity, NaN where it is none."""
+    got = f64(out)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isposinf(got), np.isposinf(want)) and \
+        np.array_equal(np.isneginf(got), np.isneginf(want))
+
+
+@pytest.mark.parametrize("T,R", SIZES)
+@pytest.mark.parametrize("wide", [False, True])
+def test_infinities_are_those_of_the_formula(T, R, wide):
+    """An infinite z gives infinities with the signs of its weights, an infinite
+    weight those of its z, whatever the other ranks hold."""
+    K, N, n = 64, 72, 3
+    d = make(T, K, N, R, n, seed=T, y_dtype=torch.float32 if wide else torch.bfloat16)
+    ids = (torch.arange(T, device=DEV) % 4 - 1).to(torch.int32)
+    d["x"][6, 3] = float("inf")                 # ids[6] = 1
+    d["x"][13, 5] = -float("inf")               # ids[13] = 0
+    d["b"][2, 7, 0] = float("inf")
+    d["b"][2, 70, R - 1] = -float("inf")
+    one = torch.ones(n, dtype=torch.int32, device=DEV)      # one rank in use: z is that infinity alone
+    for ranks in (one, None):
+        same_kind(moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"], ranks), oracle(d, ids, ranks))
+
+
+@pytest.mark.parametrize("T,R", SIZES)
+@pytest.mark.parametrize("wide", [False, True])
+def test_z_at_the_end_of_fp32(T, R, wide):
+    """z between the largest finite bf16 and the largest finite fp32 stays finite."""
+    K, N, n = 64, 72, 2
+    d = make(T, K, N, R, n, seed=T + 1, y_dtype=torch.float32 if wide else torch.bfloat16)
+    ids = torch.zeros(T, dtype=torch.int32, device=DEV)
+    top = torch.finfo(torch.bfloat16).max
+    d["a"].zero_()
+    d["a"][:, 0, 0] = 1.0
+    d["x"][:, 0] = top
+    d["scales"][:] = 1.0 + 2.0 ** -9            # z = bf16's largest x (1 + 2^-9): below 2^128 (1 - 2^-24)
+    d["b"][:, :, 0] = 0.5
+    out = f64(moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"]))
+    want = 0.5 * top * (1.0 + 2.0 ** -9)
+    # z and its product with 0.5 are exact up to z's own rounding (2^-24); the output's half step
+    assert np.all(np.abs(out - want) <= (2.0 ** -23 + (2.0 ** -24 if wide else 2.0 ** -8)) * want)
