@@ -200,10 +200,9 @@ MOE_DEV void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
 // results are, without any exchange, the first operand of step 2 with B's
 // 16-byte loads.
 //
-// RG: groups of 32 rank rows.  z is held in bf16 (half a step 2^-8 of a term that
-// is then rounded into a bf16 output); WIDE, y and out fp32: in three bf16 parts,
-// 24 significant bits (two left 1.6e-6 of the output, sixteen times fp32's error).
-// Ranks that are not in use have z = 0, whatever x holds.
+// RG: groups of 32 rank rows.  WIDE: y and out fp32.  z is held in three bf16
+// parts (adapters.cuh), one product each.  Ranks that are not in use have z = 0,
+// whatever x holds.
 constexpr int kTileCluster = 4;
 constexpr int kTileWarps = 8;
 
@@ -213,21 +212,21 @@ constexpr size_t tile_smem_bytes() {
     return (size_t)(kTileWarps / MG) * MG * MT * 4 * RG * 2 * 32 * sizeof(float2);
 }
 
-// Eight outputs of a row whose products hold a NaN, taken again in fp32 (rare: not
-// inlined).  zrow: the row's words of z, part q at q * stride (see zf below).
+// Eight outputs of a row, taken again in fp32 (a NaN among them whose z parts cannot
+// tell, see adapters.cuh; rare, so not inlined).  zrow: the row's words of z, part q
+// at q * stride (see zf below).
 template <int RG, bool WIDE>
 __device__ __noinline__ void tile_repair(const AdapterArgs& a, int t, int col, int id, int rank, const uint32_t* zrow, int stride) {
     auto z_of = [&](int r) {
         const int j = 4 * (r >> 5) + ((r >> 1) & 3);
         const uint32_t* w = zrow + (j >> 1) * 128 + ((r >> 3) & 3) * 4 + (j & 1) * 2;
         float v = 0.0f;
-        for (int q = WIDE ? 2 : 0; q >= 0; --q) v += r & 1 ? bf16_hi(w[q * stride]) : bf16_lo(w[q * stride]);
+        for (int q = kZParts - 1; q >= 0; --q) v += r & 1 ? bf16_hi(w[q * stride]) : bf16_lo(w[q * stride]);
         return v;
     };
-    const bool nan = any_nan(z_of, rank);            // a NaN in z spoils them all
     const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(a.b) + ((size_t)id * a.N + col) * a.R;
     for (int u = 0; u < 8; ++u, b += a.R) {
-        const float s = nan ? NAN : whole_product(z_of, b, rank);
+        const float s = whole_product(z_of, b, rank);
         const size_t yo = (size_t)t * a.ld_y + col + u, oo = (size_t)t * a.ld_out + col + u;
         if (WIDE) reinterpret_cast<float*>(a.out)[oo] = reinterpret_cast<const float*>(a.y)[yo] + s;
         else reinterpret_cast<__nv_bfloat16*>(a.out)[oo] = __float2bfloat16_rn(bf16_to_f(reinterpret_cast<const __nv_bfloat16*>(a.y)[yo]) + s);
@@ -238,10 +237,10 @@ template <int RG, int MT, int MG, bool WIDE>
 __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_tile(const __grid_constant__ AdapterArgs a) {
     constexpr int BT = 16 * MT * MG, PARTS = kTileWarps / MG, TJ = 4 * RG, NPASS = RG == 4 ? 2 : 1, PJ = TJ / NPASS;
     constexpr int ZN = MG * MT * TJ * 2 * 32;             // float2 values of z
-    constexpr int ZPARTS = WIDE ? 3 : 1;                  // bf16 parts that z is held in
     extern __shared__ __align__(16) float2 part_s[];      // [PARTS][ZN]; later zf in place of part 1 on
     __shared__ float s_scale[BT];
     __shared__ int s_rank[BT];                            // 0: no adapter
+    __shared__ int s_unsure[BT];                          // the row has a z that its parts may not stand for
     cg::cluster_group cl = cg::this_cluster();
     const int crank = (int)cl.block_rank();
     const int t0 = (int)(blockIdx.x / kTileCluster) * BT;
@@ -259,6 +258,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
     if (part == 0 && lane < 16 * MT) {
         s_scale[16 * MT * mg + lane] = myid >= 0 ? __ldg(a.scales + myid) : 0.0f;
         s_rank[16 * MT * mg + lane] = myrank;
+        s_unsure[16 * MT * mg + lane] = 0;
     }
     const unsigned with = __ballot_sync(0xffffffffu, myid >= 0);
     const int share = crank * PARTS + part;
@@ -358,10 +358,11 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
         v.x = left > 0 ? v.x * sc : 0.0f;
         v.y = left > 1 ? v.y * sc : 0.0f;
         const int w = ((mm * 2 * RG + (j >> 1)) * 32 + l) * 4 + (j & 1) * 2 + h;
+        uint32_t p[kZParts];
+        split_z2(v.x, v.y, p);
 #pragma unroll
-        for (int q = 0; q < ZPARTS; ++q) {
-            zf[q * ZN + w] = ZPARTS > 1 ? take_bf16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
-        }
+        for (int q = 0; q < kZParts; ++q) zf[q * ZN + w] = p[q];
+        if (z_unsure(v.x) || z_unsure(v.y)) s_unsure[16 * mm + 8 * h + (l >> 2)] = 1;
     }
     // the others may still read this CTA's sums: waited for at the end
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int q = ZPARTS - 1; q >= 0; --q) {
+                        for (int q = kZParts - 1; q >= 0; --q) {
                             const uint4* zp = zq + (size_t)(m * 2 * RG + 2 * G) * 32 + q * (ZN / 4);
                             const uint4 z0 = zp[0], z1 = zp[32];
 #pragma unroll
@@ -444,15 +445,15 @@ __global__ void __launch_bounds__(kTileWarps * 32, RG == 4 ? 1 : 2) k_adapter_ti
                 if (r0 + g + 8 * u >= a.T || col >= a.N) continue;
                 const int m = u >> 1, h = u & 1;
                 const bool own = (with >> (8 * u + g)) & 1u;          // rows without an adapter keep y's bits
-                bool odd = false;
-                if (own && ZPARTS > 1) {
+                const int row = r0 + g + 8 * u - t0;
+                if (own && s_unsure[row]) {
+                    bool nan = false;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) odd = odd || delta[m][j][2 * h] != delta[m][j][2 * h] || delta[m][j][2 * h + 1] != delta[m][j][2 * h + 1];
-                }
-                if (odd) {
-                    const int t = r0 + g + 8 * u, row = t - t0;
-                    tile_repair<RG, WIDE>(a, t, col, __ldg(a.ids + t), s_rank[row], zf + ((row >> 4) * 2 * RG * 32 + 4 * g) * 4 + h, ZN);
-                    continue;
+                    for (int j = 0; j < 4; ++j) nan = nan || delta[m][j][2 * h] != delta[m][j][2 * h] || delta[m][j][2 * h + 1] != delta[m][j][2 * h + 1];
+                    if (nan) {
+                        tile_repair<RG, WIDE>(a, t0 + row, col, __ldg(a.ids + t0 + row), s_rank[row], zf + ((row >> 4) * 2 * RG * 32 + 4 * g) * 4 + h, ZN);
+                        continue;
+                    }
                 }
                 const size_t off = (size_t)(r0 + g + 8 * u) * a.ld_out + col;
                 uint32_t* y = &yv[u][0].x;

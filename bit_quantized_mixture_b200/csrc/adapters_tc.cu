@@ -11,18 +11,20 @@
 //      one pass).
 //   2. The cluster's partial sums: each CTA owns 128 / CL of the rows; the others
 //      write their sums for these into its shared memory, it adds them (in the
-//      CTAs' order), and writes z times its scale as the bf16 operand of step 3
-//      into every CTA's.  All remote traffic is stores, whose latency nobody
-//      waits for (reading the others' sums took 5 to 8 us of a tile's 30).
+//      CTAs' order), and writes z times its scale as the operand of step 3 (three
+//      bf16 parts, adapters.cuh) into every CTA's: at ranks above 16 in the place of
+//      the sums, when all CTAs have read theirs (operand and sums side by side leave
+//      the rings of x and y two slots in place of three: 8192 tokens of one
+//      request, rank 16, 29 us against 27).  All remote traffic is stores, whose
+//      latency nobody waits for (reading the others' sums took 5 to 8 us of a tile's
+//      30).
 //   3. out: per chunk of 64 (fp32: 32) output columns and adapter of the tile, one
 //      accumulator of Z B_i^T; rows of that adapter add it to their y, which TMA
 //      brought into the same ring that x came through (it fills while the sums
 //      of step 2 meet), and TMA stores the chunk.
 //
 // A row's results come from its own adapter's accumulators alone, so weights that
-// are not finite spoil no other adapter's tokens.  z is held in bf16 (half a step
-// 2^-8 of a term that is then rounded into a bf16 output), for fp32 outputs in three
-// bf16 parts (24 significant bits).
+// are not finite spoil no other adapter's tokens.
 //
 // Warps: 0 loads x and y, 11-12 A and B (TMA; one thread for all of it spends longer on
 // its waits and loads than a chunk takes), 1-2 MMA issuers, 3-10 epilogue (two groups
@@ -64,13 +66,17 @@ struct TcCfg {
     static constexpr int BIG = kTcRows * 128;               // a chunk of x or y
     static constexpr int SMALL = RB * 64 * 128;             // a chunk of one A, or of one B
     // slots of each stream's rings
-    static constexpr int NBIG = RB == 1 ? (WIDE ? 2 : 3) : 2, NSMALL = RB == 1 ? 4 : 1;
+    static constexpr int NBIG = RB == 1 ? 3 : 2, NSMALL = RB == 1 ? 4 : 1;
     static constexpr int OFF_SMALL = kTcStreams * NBIG * BIG;
-    static constexpr int OFF_Z = OFF_SMALL + kTcStreams * NSMALL * SMALL;        // fp32 sums of the rows that this CTA owns, by source CTA
-    static constexpr int ZBLOCK = kTcRows * 128;                    // 64 columns of the bf16 operand
-    static constexpr int OFF_OP = OFF_Z + RB * 64 * kTcRows * 4;
-    static constexpr int PARTS = WIDE ? 3 : 1;                      // bf16 parts that z is held in
-    static constexpr size_t BYTES = OFF_OP + RB * PARTS * ZBLOCK + 1024;   // base rounded up to the swizzle's 1024
+    // fp32 sums of the rows that this CTA owns, by source CTA; the second product's
+    // operand lies behind as many of them as there is room for, and otherwise in
+    // their place once they are read
+    static constexpr int OFF_Z = OFF_SMALL + kTcStreams * NSMALL * SMALL, OFF_OP = OFF_Z + (RB == 1 ? 15 * 1024 : 0);
+    static constexpr int SUMS = RB * 64 * kTcRows * 4;
+    static constexpr int ZBLOCK = kTcRows * 128;                    // 64 columns of a part of the operand
+    static constexpr int OPERAND = RB * kZParts * ZBLOCK;
+    static_assert(OFF_OP + OPERAND >= OFF_Z + SUMS, "the sums end within the operand");
+    static constexpr size_t BYTES = OFF_OP + OPERAND + 1024;        // base rounded up to the swizzle's 1024
 };
 
 struct TcMaps {
@@ -144,22 +150,21 @@ MOE_DEV void wait_some(uint64_t* bar, uint32_t parity) {
 // where a call without an error word of its own records a wait that gave up
 __device__ int g_wait_err;
 
-// 32 output columns of a row whose products hold a NaN, taken again in fp32 (rare:
-// not inlined): n: the first column's number, c: its place in the chunk at `tile`
-// (which holds y), op: z's parts
+// 32 output columns of a row, taken again in fp32 (a NaN among them whose z parts
+// cannot tell, see adapters.cuh; rare, so not inlined).  n: the first column's
+// number, c: its place in the chunk at `tile` (which holds y), op: z's parts
 template <int RB, bool WIDE>
 __device__ __noinline__ void tc_repair(const AdapterArgs& a, int id, int rank, int n, int row, uint8_t* tile, int c, const uint8_t* op) {
     using C = TcCfg<RB, WIDE>;
     auto z_of = [&](int r) {
         float v = 0.0f;
-        for (int h = C::PARTS - 1; h >= 0; --h)
+        for (int h = kZParts - 1; h >= 0; --h)
             v += bf16_to_f(*reinterpret_cast<const __nv_bfloat16*>(op + (h * RB + (r >> 6)) * C::ZBLOCK + sw_piece(row, (r & 63) >> 3) + (r & 7) * 2));
         return v;
     };
-    const bool nan = any_nan(z_of, rank);            // a NaN in z spoils them all
     const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(a.b) + ((size_t)id * a.N + n) * a.R;
     for (int u = 0; u < 32 && n + u < a.N; ++u, b += a.R) {
-        const float s = nan ? NAN : whole_product(z_of, b, rank);
+        const float s = whole_product(z_of, b, rank);
         if (WIDE) {
             float* p = reinterpret_cast<float*>(tile + sw_piece(row, (c + u) >> 2)) + ((c + u) & 3);
             *p += s;
@@ -178,7 +183,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t big_full[kTcStreams][NBIG], big_empty[kTcStreams][NBIG], chunk_done[kTcStreams][NBIG];
     __shared__ uint64_t small_full[kTcStreams][NSMALL], small_empty[kTcStreams][NSMALL], small_clean[kTcStreams][NSMALL];
-    __shared__ uint64_t z_full, z_free, z_ready, op_full;
+    __shared__ uint64_t z_full, z_free, z_ready, z_read, op_full;
     __shared__ uint64_t d_full[kTcStreams][kTcDBufs], d_empty[kTcStreams][kTcDBufs];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -245,6 +250,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         mbar_init(&z_full, (uint32_t)min(kTcStreams, k1 - k0));
         mbar_init(&z_free, kTcEpiWarps);
         mbar_init(&z_ready, (uint32_t)(kTcEpiWarps * CL));
+        mbar_init(&z_read, (uint32_t)(kTcEpiWarps * CL));
         mbar_init(&op_full, (uint32_t)(kTcEpiWarps * CL));
         abort_flag = 0;
         fence_barrier_init();
@@ -388,10 +394,15 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                     tc_fence_after();
                     const uint64_t bd = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
                     const uint32_t dst = tmem + kTcZCols + 64u * (uint32_t)(w * kTcDBufs + buf);
-                    for (int h = 0; h < C::PARTS; ++h)
-                        for (int q = 0; q < steps; ++q)
-                            mma_bf16(dst, dz + (uint64_t)((h * RB + (q >> 2)) * (C::ZBLOCK >> 4) + 2 * (q & 3)),
-                                     bd + (uint64_t)((q >> 2) * (NC * 128 >> 4) + 2 * (q & 3)), ido, h + q > 0 ? 1u : 0u);
+                    // (unrolled: rank 64, 16 requests, 8192 tokens 49.7 -> 44.8 us)
+#pragma unroll
+                    for (int q = 0; q < 4 * RB; ++q)
+                        if (q < steps) {
+#pragma unroll
+                            for (int h = 0; h < kZParts; ++h)
+                                mma_bf16(dst, dz + (uint64_t)((h * RB + (q >> 2)) * (C::ZBLOCK >> 4) + 2 * (q & 3)),
+                                         bd + (uint64_t)((q >> 2) * (NC * 128 >> 4) + 2 * (q & 3)), ido, h + q > 0 ? 1u : 0u);
+                        }
                     mma_commit(&small_empty[w][small.slot]);
                     mma_commit(&d_full[w][buf]);
                 }
@@ -511,32 +522,47 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                 ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_ready, 0u, &abort_flag, err, 52));
             }
             if (ok) {
-                uint8_t* op = smem + C::OFF_OP;
-                for (int i = (int)threadIdx.x - 96; i < own_rows * (rows_a / 8); i += kTcEpiWarps * 32) {
-                    const int rl = i % own_rows, j = i / own_rows, r = crank * own_rows + rl;     // row, eight columns
-                    float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    const int rid = s_id[r];
-                    if (rid >= 0) {
-                        const int rank = rank_of(rid);
-                        const float scale = s_scale[r];
-                        for (int q = 0; q < CL; ++q) {
-                            const float4 v0 = zp[(q * quads + 2 * j) * own_rows + rl], v1 = zp[(q * quads + 2 * j + 1) * own_rows + rl];
-                            z[0] += v0.x; z[1] += v0.y; z[2] += v0.z; z[3] += v0.w;
-                            z[4] += v1.x; z[5] += v1.y; z[6] += v1.z; z[7] += v1.w;
-                        }
+                // this CTA's rows, eight columns of one at a time: summed and scaled in
+                // registers, written when nobody needs the sums any more
+                constexpr int ITEMS = kTcRows * RB * 8 / (kTcEpiWarps * 32);
+                const int items = own_rows * (rows_a / 8), i0 = (int)threadIdx.x - 96;
+                float z[ITEMS][8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) z[q] = 8 * j + q < rank ? z[q] * scale : 0.0f;
+                for (int u = 0; u < ITEMS; ++u) {
+                    const int i = i0 + u * kTcEpiWarps * 32, rl = i % own_rows, j = i / own_rows, r = crank * own_rows + rl;     // row, eight columns
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) z[u][q] = 0.0f;
+                    if (i >= items || s_id[r] < 0) continue;
+                    const int rank = rank_of(s_id[r]);
+                    const float scale = s_scale[r];
+                    for (int q = 0; q < CL; ++q) {
+                        const float4 v0 = zp[(q * quads + 2 * j) * own_rows + rl], v1 = zp[(q * quads + 2 * j + 1) * own_rows + rl];
+                        z[u][0] += v0.x; z[u][1] += v0.y; z[u][2] += v0.z; z[u][3] += v0.w;
+                        z[u][4] += v1.x; z[u][5] += v1.y; z[u][6] += v1.z; z[u][7] += v1.w;
                     }
-                    uint8_t* d = op + (j >> 3) * C::ZBLOCK + sw_piece(r, j & 7);
 #pragma unroll
-                    for (int h = 0; h < C::PARTS; ++h, d += RB * C::ZBLOCK) {
-                        uint32_t w[4];
+                    for (int q = 0; q < 8; ++q) z[u][q] = 8 * j + q < rank ? z[u][q] * scale : 0.0f;
+                }
+                if (C::OFF_Z + rows_a * kTcRows * 4 > C::OFF_OP) {       // the operand takes their place
+                    __syncwarp();
+                    if (lane < CL) mbar_arrive_cluster(&z_read, lane);
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_read, 0u, &abort_flag, err, 53));
+                }
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = C::PARTS > 1 ? take_bf16x2(z[2 * q], z[2 * q + 1]) : pack_bf16x2(z[2 * q], z[2 * q + 1]);
-                        for (int q = 0; q < CL; ++q) st_cluster_v4(d, q, make_uint4(w[0], w[1], w[2], w[3]));
+                for (int u = 0; u < ITEMS; ++u) {
+                    const int i = i0 + u * kTcEpiWarps * 32, j = i / own_rows, r = crank * own_rows + i % own_rows;
+                    if (!ok || i >= items) continue;
+                    uint32_t w[4][kZParts];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) split_z2(z[u][2 * q], z[u][2 * q + 1], w[q]);
+#pragma unroll
+                    for (int h = 0; h < kZParts; ++h) {
+                        uint8_t* d = smem + C::OFF_OP + (h * RB + (j >> 3)) * C::ZBLOCK + sw_piece(r, j & 7);
+                        for (int q = 0; q < CL; ++q) st_cluster_v4(d, q, make_uint4(w[0][h], w[1][h], w[2][h], w[3][h]));
                     }
                 }
+            }
+            if (ok) {
                 asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
                 __syncwarp();
                 if (lane < CL) mbar_arrive_cluster(&op_full, lane);
@@ -546,6 +572,16 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         // use from the next), and this group's chunks, every other one, go on
         // where its stream left off.
         if (D == 0) ok = all_wait(&z_full, 0u, &abort_flag, err, 58);
+        bool unsure = false;                 // this row has a z that its parts may not stand for
+        if (ok && D > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 60));
+            for (int j = 0; ok && j < rows_a / 8; ++j) {
+                const uint4 p = *reinterpret_cast<const uint4*>(smem + C::OFF_OP + (j >> 3) * C::ZBLOCK + sw_piece(row, j & 7));
+                const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) unsure = unsure || z_unsure(bf16_lo(w[q])) || z_unsure(bf16_hi(w[q]));
+            }
+        }
         int unit = 0, big = passes * count(k0, k1, group);
         Turned at(n0, n1, turn);
         if (group) at.next();
@@ -564,10 +600,12 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                     for (int c = 0; c < NC; c += 32) {
                         uint32_t r[32];
                         tmem_ld_x32c(src + (uint32_t)c, r);
-                        if (mine == d && C::PARTS > 1 && sum_is_nan(r)) {
-                            // (the operand is complete; this thread has not seen it yet)
-                            if (mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 53))
-                                tc_repair<RB, WIDE>(a, id, s_rank[d], NC * at.at + c, row, tile, c, smem + C::OFF_OP);
+                        bool nan = false;
+                        if (unsure)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) nan = nan || __uint_as_float(r[e]) != __uint_as_float(r[e]);
+                        if (mine == d && nan) {
+                            tc_repair<RB, WIDE>(a, id, s_rank[d], NC * at.at + c, row, tile, c, smem + C::OFF_OP);
                         } else if (mine == d) {
 #pragma unroll
                             for (int j = 0; j < (WIDE ? 8 : 4); ++j) {

@@ -371,9 +371,8 @@ typedef struct {
  * whose id lies outside [0, n), or whose adapter has rank 0, keeps y_t bit
  * for bit.  x bf16 [T, K]; y and out [T, N], both bf16 or (y_fp32) both
  * fp32; out may be y itself (same ld) and otherwise overlaps no input.
- * Products and sums are fp32, out is rounded once.  With more than a few
- * tokens the second product's operand, scale * a x, is held in bf16 for bf16
- * outputs and in three bf16 parts (24 significant bits) for fp32 outputs.
+ * Products and sums are fp32, scale * a x is held in 24 significant bits, out
+ * is rounded once.
  * Deterministic; needs no workspace.
  * Errors: INVALID_ARG, UNSUPPORTED (R, K, N or T), CUDA. */
 moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,

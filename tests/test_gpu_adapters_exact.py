@@ -38,6 +38,7 @@ def test_infinities_are_those_of_the_formula(T, R, wide):
     ids = (torch.arange(T, device=DEV) % 4 - 1).to(torch.int32)
     d["x"][6, 3] = float("inf")                 # ids[6] = 1
     d["x"][13, 5] = -float("inf")               # ids[13] = 0
+    d["x"][11] *= 2.0 ** -115                   # ids[11] = 2: a z far below one
     d["b"][2, 7, 0] = float("inf")
     d["b"][2, 70, R - 1] = -float("inf")
     one = torch.ones(n, dtype=torch.int32, device=DEV)      # one rank in use: z is that infinity alone
@@ -62,3 +63,28 @@ def test_z_at_the_end_of_fp32(T, R, wide):
     want = 0.5 * top * (1.0 + 2.0 ** -9)
     # z and its product with 0.5 are exact up to z's own rounding (2^-24); the output's half step
     assert np.all(np.abs(out - want) <= (2.0 ** -23 + (2.0 ** -24 if wide else 2.0 ** -8)) * want)
+
+
+@pytest.mark.parametrize("T,R", SIZES + [(1600, 72), (2310, 64), (2000, 40)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_z_is_held_in_fp32_for_either_output(T, R, wide):
+    """Outputs that nearly cancel, y = -delta rounded, show every rounding before
+    the last.  z sums K products (chains of at most K/16 + 16 fp32 steps, each off
+    by at most 2^-23 of the running magnitude), is scaled (2^-24) and held in 24
+    bits; the second product sums R terms in three parts (3 R/16 + 18 steps), y is
+    added (2^-23) and the output rounded (half a step)."""
+    K, N, n = 64, 72, 3
+    d = make(T, K, N, R, n, seed=2 * T + R, y_dtype=torch.float32 if wide else torch.bfloat16)
+    ids = (torch.arange(T, device=DEV) * n // T).to(torch.int32)
+    x, a, b, s = (f64(d[i]) for i in ("x", "a", "b", "scales"))
+    own = ids.cpu().numpy()
+    z = s[own][:, None] * np.einsum("tk,trk->tr", x, a[own])
+    delta = np.einsum("tr,tnr->tn", z, b[own])
+    d["y"] = torch.from_numpy(-delta).to(DEV).to(d["y"].dtype)
+    y = f64(d["y"])
+    got = f64(moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"]))
+    zabs = np.abs(s[own])[:, None] * np.einsum("tk,trk->tr", np.abs(x), np.abs(a[own]))
+    ez = 2.0 ** -23 * (K / 16 + 16) * zabs + 2.0 ** -23 * np.abs(z)
+    tol = np.einsum("tr,tnr->tn", ez + 2.0 ** -23 * (3 * R / 16 + 18) * np.abs(z), np.abs(b[own])) + 2.0 ** -23 * np.abs(y)
+    tol += (2.0 ** -24 if wide else 2.0 ** -8) * (np.abs(y + delta) + tol)
+    assert np.all(np.abs(got - (y + delta)) <= tol), np.max(np.abs(got - (y + delta)) / tol)
