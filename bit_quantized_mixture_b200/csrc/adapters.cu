@@ -30,14 +30,16 @@ constexpr int kAdTokenMax = 256, kAdTokenWork = 8192;        // most tokens, mos
 // 5.6 / 5.4 / 7.1; 128 tokens 9.8 / 6.4 / 7.6; 256 tokens 18 / 11.4 / 9.4.
 constexpr int kAdCluster8 = 32, kAdCluster4 = 192;           // up to so many tokens 8, 4 CTAs
 // 2048 -> 2048, 12 requests in order, us, tiles of 16 tokens / of 128 on tcgen05
-// (adapters_tc.cu), bf16: rank 16, 2000 tokens 14.5 / 21, 2800 tokens 20.3 / 20.3, 8192
-// tokens 53 / 31; rank 64, 2000 tokens 23 / 25, 2300 tokens 26.2 / 25.6, 8192 tokens
-// 75 / 39; rank 128, 1000 tokens 29.6 / 31, 1500 tokens 42 / 34, 8192 tokens 183 / 65.
-// fp32 outputs (three parts of z), tiles of 16 / of 64 / tcgen05: rank 16, 3300 tokens
-// 28 / 31 / 34, 4096 tokens 34 / 32 / 33, 8192 tokens 63 / 52 / 48; rank 64, 3300 tokens
-// 39 / 54 / 43, 8192 tokens 87 / 81 / 71.
-constexpr int kAdTc32 = 2800, kAdTc64 = 2300, kAdTc128 = 1500;   // from so many tokens on tcgen05: ranks to 32, 64, 128
-constexpr int kAdSmallWide = 3600, kAdTcWide = 8192;             // fp32: up to so many in tiles of 16, from so many on tcgen05
+// (adapters_tc.cu), bf16: rank 16, 2800 tokens 22.3 / 24.1, 3700 tokens 29.5 / 28.1, 8192
+// tokens 58 / 35; rank 64, 2500 tokens 31.2 / 33.2, 2800 tokens 34 / 31.4, 8192 tokens
+// 82 / 44; rank 128, 1000 tokens 33 / 42, 1300 tokens 42.3 / 41.7, 8192 tokens 200 / 82.
+// fp32 outputs, tiles of 16 / of 64 / tcgen05: rank 16, 3700 tokens 33 / 36 / 38, 4500
+// tokens 37 / 32 / 49, 6000 tokens 49 / 49 / 51, 8192 tokens 65 / 55 / 48; rank 64, 4500
+// tokens 51 / 52 / 62, 6000 tokens 67 / 77 / 58, 8192 tokens 88 / 83 / 60; rank 128
+// (no tcgen05), 3200 tokens 90 / 94, 3700 tokens 102 / 87, 8192 tokens 202 / 152.
+constexpr int kAdTc32 = 3200, kAdTc64 = 2700, kAdTc128 = 1300;   // from so many tokens on tcgen05: ranks to 32, 64, 128
+constexpr int kAdTcWide32 = 7000, kAdTcWide64 = 5000;            // fp32, likewise
+constexpr int kAdTile64Wide32 = 4000, kAdTile64Wide128 = 3600;   // fp32: from so many on tiles of 64 (ranks 33 to 64: never)
 constexpr int kAdThreads = 256;
 
 MOE_DEV float dot8(const uint4& p, const uint4& q, float s) {
@@ -502,11 +504,11 @@ cudaError_t launch_tile(const AdapterArgs& a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, k_adapter_tile<RG, MT, MG, WIDE>, a);
 }
 
-template <int MT, int MG, bool WIDE>
+template <bool WIDE>
 cudaError_t launch_tiles(const AdapterArgs& a, cudaStream_t st) {
-    if (a.R <= 32) return launch_tile<1, MT, MG, WIDE>(a, st);
-    if (a.R <= 64) return launch_tile<2, MT, MG, WIDE>(a, st);
-    return launch_tile<4, MT, MG, WIDE>(a, st);
+    if (a.R <= 32) return launch_tile<1, 1, 1, WIDE>(a, st);
+    if (a.R <= 64) return launch_tile<2, 1, 1, WIDE>(a, st);
+    return launch_tile<4, 1, 1, WIDE>(a, st);
 }
 
 }  // namespace
@@ -516,12 +518,15 @@ cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st) {
         if (a.T <= kAdCluster8) return launch_tokens<8>(a, st);
         return a.T <= kAdCluster4 ? launch_tokens<4>(a, st) : launch_tokens<2>(a, st);
     }
-    if (a.T >= (a.wide ? kAdTcWide : a.R <= 32 ? kAdTc32 : a.R <= 64 ? kAdTc64 : kAdTc128)) {
+    const int tc = a.R <= 32 ? (a.wide ? kAdTcWide32 : kAdTc32) : a.R <= 64 ? (a.wide ? kAdTcWide64 : kAdTc64) : kAdTc128;
+    if (a.T >= tc) {
         const cudaError_t e = launch_add_adapters_tc(a, st);
         if (e != cudaErrorNotSupported) return e;
     }
-    if (!a.wide) return launch_tiles<1, 1, false>(a, st);
-    return a.T <= kAdSmallWide ? launch_tiles<1, 1, true>(a, st) : launch_tiles<2, 2, true>(a, st);
+    if (!a.wide) return launch_tiles<false>(a, st);
+    if (a.R <= 32 && a.T >= kAdTile64Wide32) return launch_tile<1, 2, 2, true>(a, st);
+    if (a.R > 64 && a.T >= kAdTile64Wide128) return launch_tile<4, 2, 2, true>(a, st);
+    return launch_tiles<true>(a, st);
 }
 
 }  // namespace moe

@@ -728,7 +728,7 @@ cudaError_t take_wait_error(int* code) {
 
 cudaError_t launch_add_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
     if (a.R <= 64) return a.wide ? launch_tc<1, true>(a, st) : launch_tc<1, false>(a, st);
-    // ranks above 64 with fp32 outputs: sums, operand halves and rings do not fit
+    // ranks above 64 with fp32 outputs have no variant here
     return a.wide ? cudaErrorNotSupported : launch_tc<2, false>(a, st);
 }
 

@@ -6,7 +6,7 @@ import torch
 
 from bit_quantized_mixture_b200 import moe
 from oracle import moe_oracle as O
-from tests.test_gpu_adapters import DEV, f64, make
+from tests.test_gpu_adapters import DEV, assert_close, f64, make
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,15 @@ def test_z_is_held_in_fp32_for_either_output(T, R, wide):
     tol = np.einsum("tr,tnr->tn", ez + 2.0 ** -23 * (3 * R / 16 + 18) * np.abs(z), np.abs(b[own])) + 2.0 ** -23 * np.abs(y)
     tol += (2.0 ** -24 if wide else 2.0 ** -8) * (np.abs(y + delta) + tol)
     assert np.all(np.abs(got - (y + delta)) <= tol), np.max(np.abs(got - (y + delta)) / tol)
+
+
+@pytest.mark.parametrize("T,R,wide", [(1299, 72, False), (1300, 128, False), (2699, 64, False), (2700, 40, False), (3199, 32, False), (3200, 8, False),
+                                      (3999, 16, True), (4000, 32, True), (6999, 8, True), (7000, 24, True), (4999, 64, True), (5000, 40, True),
+                                      (3599, 72, True), (3600, 128, True)])
+def test_both_sides_of_each_token_count_that_changes_the_kernel(T, R, wide):
+    K, N, n = 136, 72, 5
+    d = make(T, K, N, R, n, seed=T + R, y_dtype=torch.float32 if wide else torch.bfloat16)
+    g = torch.Generator().manual_seed(T)
+    ids = torch.randint(-1, n, (T,), generator=g).sort().values.to(torch.int32).to(DEV)
+    ranks = torch.randint(1, R + 1, (n,), generator=g).to(torch.int32).to(DEV)
+    assert_close(moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"], ranks), d, ids, ranks)
