@@ -45,10 +45,10 @@ constexpr int kSelCand = 64;         // candidates that a warp's list holds
 constexpr int kSelSpare = 4;         // ... and may hold beyond k of the lanes' largest keys
 
 // the largest of a warp's values (redux.sync on fp32: one instruction in place of
-// five shuffles and five maxima)
+// five shuffles and five maxima; volatile, since every lane has to come to it)
 MOE_DEV float warp_max1(float v) {
     float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
 // exp by the approximate power of two, with __expf's error; results below 2^-126 are
