@@ -25,3 +25,10 @@ def test_collectives_are_volatile():
     into a branch that some of them do not take, it would wait for them."""
     found = [(at, code) for at, volatile, code in statements() if re.search(r"\.sync\b|barrier\.|\bbar\.", code) and not volatile]
     assert not found
+
+
+def test_tensor_memory_loads_end_with_their_wait():
+    """The load writes its registers until the wait; as a statement of its own, the
+    wait would not keep what reads them behind it."""
+    found = [(at, code) for at, _, code in statements() if "tcgen05.ld" in code and "tcgen05.wait::ld" not in code.split("tcgen05.ld")[-1]]
+    assert not found
