@@ -2,7 +2,7 @@
 // that takes part in the selection only, groups of experts, top-k, and the
 // chosen experts' weights (renormalised or not, times a scale).
 //
-//   s_e   = softmax over the eligible experts, or 1 / (1 + exp(-l_e))
+//   s_e   = softmax over the row's logits, or 1 / (1 + exp(-l_e))
 //   key_e = s_e + bias_e; without a bias the order of the logits
 //   group score = largest key, or sum of the two largest; the best groups stay
 //   ids   = the k best keys of the groups that stay, key descending, expert
@@ -70,7 +70,8 @@ MOE_DEV double warp_max_d(double v) {
 }
 
 // NaN, -inf and the lowest finite value (what masks are filled with) switch
-// an expert off, as a logit or as a bias; +inf counts as the largest one.
+// an expert off: as a logit altogether, as a bias for the selection (its score
+// stays in the softmax's sum); +inf counts as the largest one.
 MOE_DEV bool sel_on(float v) { return v > -FLT_MAX; }
 MOE_DEV float sel_cap(float v) { return fminf(v, FLT_MAX); }
 
@@ -114,13 +115,13 @@ struct SelTeam {
     bool fail;
 };
 
-// sum of exp(l - top) over the eligible experts in fp64 (softmax)
+// sum of exp(l - top) over the row in fp64 (softmax)
 MOE_DEV double softmax_total(const SelectArgs& a, const float* row, float top) {
     double total = 0.0;
     if (!a.sigmoid)
         for (int e = threadIdx.x & 31; e < a.E; e += 32) {
             const float l = __ldg(row + e);
-            if (sel_on(l) && (!a.bias || sel_on(__ldg(a.bias + e)))) total += exp((double)sel_cap(l) - (double)top);
+            if (sel_on(l)) total += exp((double)sel_cap(l) - (double)top);
         }
     return warp_sum_d(total);
 }
@@ -144,7 +145,7 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
         key[i] = -INFINITY;
         if (e < a.E) {
             const float l = __ldg(row + e);
-            if (sel_on(l) && (!a.bias || sel_on(__ldg(a.bias + e)))) {
+            if (sel_on(l)) {
                 key[i] = (double)sel_cap(l);
                 top = fmaxf(top, sel_cap(l));
                 any = true;
@@ -165,7 +166,10 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
     if (a.bias)
 #pragma unroll 1
         for (int i = 0; i < SLOTS; ++i)
-            if (key[i] > -INFINITY) key[i] = score(key[i]) + (double)sel_cap(__ldg(a.bias + lane + 32 * i));
+            if (key[i] > -INFINITY) {
+                const float b = __ldg(a.bias + lane + 32 * i);
+                key[i] = sel_on(b) ? score(key[i]) + (double)sel_cap(b) : -INFINITY;
+            }
     if (a.G > 1) {
         // lane g: group g's score
         double mine = -INFINITY;
@@ -480,7 +484,7 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
             for (int q = 0; q < 4; ++q) d[q] = e + q < a.E ? __ldg(p + e + q) : off;
         }
     };
-    float v[SLOTS];                                  // eligible: above -FLT_MAX
+    float v[SLOTS];                                  // on: above -FLT_MAX
 #pragma unroll
     for (int i = 0; i < CH; ++i) load4(row, first(i), -FLT_MAX, v + 4 * i);
 #pragma unroll
@@ -490,15 +494,6 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
     float top = -FLT_MAX, total = 1.0f, ks = 1e-6f;
     if (!a.sigmoid && (scored || !a.renorm)) {
         float s = 0.0f;
-        if (a.bias) {                                // experts that their bias switches off leave the softmax
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                float b[4];
-                load4(a.bias, first(i), -FLT_MAX, b);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[4 * i + q] = sel_on(b[q]) ? v[4 * i + q] : -FLT_MAX;
-            }
-        }
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) top = fmaxf(top, v[i]);
         top = warp_max1(top);

@@ -316,7 +316,8 @@ moe_status moe_set_expert_table(moe_handle h, const void* const* blocks, moe_str
  *   eligible: l_e and bias_e are above the lowest finite fp32 value: NaN,
  *             -inf and that value (as masks hold them) switch an expert off;
  *             +inf counts as the largest finite value
- *   s_e   = softmax over the eligible experts, or 1 / (1 + exp(-l_e))
+ *   s_e   = softmax over the row (logits that are off left out; a bias takes no
+ *           part in it, not even one that is off), or 1 / (1 + exp(-l_e))
  *   key_e = s_e + bias_e; without a bias the keys' order is the logits' order
  *   groups of E / num_groups consecutive experts; the top_groups best by
  *           group_score stay (the lower group on ties, groups without an

@@ -527,14 +527,15 @@ def select_experts(logits, k, score="softmax", bias=None, num_groups=1, top_grou
                    scale=1.0):
     """Expert ids [T, k] and fp64 weights of fp32 logits [T, E] under a routing
     rule.  NaN, -inf and the lowest finite fp32 value switch an expert off (as
-    a logit or as a bias); +inf counts as the largest finite value."""
+    a logit altogether, as a bias for the selection alone: its score stays in the
+    softmax's sum); +inf counts as the largest finite value."""
     logits = np.asarray(logits, dtype=np.float64)
     T, E = logits.shape
     ids = np.zeros((T, k), dtype=np.int32)
     w = np.zeros((T, k))
     per = E // num_groups
     for t in range(T):
-        on = [e for e in range(E) if logits[t, e] > -F32_MAX and (bias is None or float(bias[e]) > -F32_MAX)]
+        on = [e for e in range(E) if logits[t, e] > -F32_MAX]
         x = {e: min(logits[t, e], F32_MAX) for e in on}
         if score == "sigmoid":
             s = {e: (1.0 / (1.0 + np.exp(-x[e])) if x[e] > -700 else 0.0) for e in on}
@@ -543,6 +544,8 @@ def select_experts(logits, k, score="softmax", bias=None, num_groups=1, top_grou
             ex = {e: np.exp(x[e] - top) for e in on}
             total = sum(ex.values())
             s = {e: ex[e] / total for e in on}
+        if bias is not None:
+            on = [e for e in on if float(bias[e]) > -F32_MAX]
         key = {e: (x[e] if bias is None else s[e] + min(float(bias[e]), F32_MAX)) for e in on}
         if num_groups > 1:
             value = {}

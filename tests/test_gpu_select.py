@@ -105,6 +105,28 @@ def test_masks(score, G, renorm):
             check(L, k, b, score=score, num_groups=G, top_groups=max(1, G // 2), group_score=gs, renorm=renorm)
 
 
+@pytest.mark.parametrize("E,G,keep", [(48, 1, 1), (48, 4, 2), (600, 24, 5), (1024, 1, 1)])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_a_bias_that_is_off_changes_no_score(E, G, keep, group_score):
+    """Unnormalised softmax weights of the experts that are left are those of the
+    whole row, also where the ones switched off hold nearly all of it, in rows
+    decided in fp32 and (equal keys) in fp64, and in rows with more equal
+    keys than a list holds."""
+    k = 6
+    rng = np.random.default_rng(E + G)
+    L = rng.standard_normal((12, E)).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    bias[::5] = -np.inf
+    bias[1::7] = np.nan
+    L[1, ::5] += 20.0
+    L[2] = 0.5
+    L[3, 1::7] = -np.inf
+    check(L, k, bias, renorm=False, scale=2.5, num_groups=G, top_groups=keep, group_score=group_score)
+    bias = np.where(np.arange(E) % 5 == 0, -np.inf, 0.25).astype(np.float32)
+    L[4:8] = np.float32(0.25) * rng.integers(-1, 2, size=(4, E))
+    check(L, k, bias, renorm=False, num_groups=G, top_groups=keep, group_score=group_score)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_extreme_logits(score):
     """Scores that underflow or saturate: the order stays the logits' and

@@ -44,6 +44,15 @@ def test_selection_masks():
     assert w.tolist() == [[1.0, 0.0], [0.0, 0.0], [0.5, 0.5]]
 
 
+def test_a_bias_takes_no_part_in_the_scores():
+    """Softmax scores 1/2, 1/4, 1/4; a bias that switches expert 0 off leaves the
+    others theirs."""
+    L = np.array([[math.log(2), 0.0, 0.0]], dtype=np.float32)
+    for off in (-np.inf, np.nan, -F32_MAX):
+        ids, w = O.select_experts(L, 2, bias=np.array([off, 0, 0.5], dtype=np.float32), renorm=False, scale=4.0)
+        assert ids.tolist() == [[2, 1]] and np.allclose(w, [[1.0, 1.0]], atol=1e-7)
+
+
 def test_adapters_worked_example():
     x = np.array([[1.0, 2.0], [3.0, 4.0], [5.0, 6.0]])
     y = np.array([[10.0], [20.0], [30.0]])
