@@ -5,10 +5,13 @@
 //   s_e   = softmax over the row's logits, or 1 / (1 + exp(-l_e))
 //   key_e = s_e + bias_e; without a bias the order of the logits
 //   group score = largest key, or sum of the two largest; the best groups stay
-//   ids   = the k best keys of the groups that stay, key descending, expert
-//           ascending on equal keys; w_j = s_j [/ sum s] * scale
+//   ids   = the k best keys of the groups that stay, key descending, then logit
+//           descending, then expert ascending; w_j = s_j [/ sum s] * scale
 //
-// The order is that of the exact keys.  fp32 keys alone would swap about one
+// The order is that of the keys in fp64.  Scores rise with their logits, so where
+// two keys are equal there (saturated scores, scores far below their biases) the
+// logits tell the rest: a bias of one value for all experts changes no order.  fp32
+// keys alone would swap about one
 // token's experts in a few thousand, and fp64 keys for every expert bind the
 // kernel to the fp64 exponentials (123 us for 8192 tokens of 512 experts).  So
 // select_fast works in fp32 with a bound on each key's error.  Where the last
@@ -171,15 +174,19 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
                 key[i] = sel_on(b) ? score(key[i]) + (double)sel_cap(b) : -INFINITY;
             }
     if (a.G > 1) {
-        // lane g: group g's score
+        // lane g: group g's score, and the logit of its largest key
         double mine = -INFINITY;
+        float minel = -INFINITY;
         for (int g = 0; g < a.G; ++g) {
             double b1 = -INFINITY, b2 = -INFINITY;
+            float bl = -INFINITY;
 #pragma unroll 1
             for (int i = 0; i < SLOTS; ++i) {
                 const int e = lane + 32 * i;
                 if (e < a.E && e / a.per == g && key[i] > -INFINITY) {
                     const double v = scored_groups && !a.bias ? score(key[i]) : key[i];
+                    const float l = sel_cap(__ldg(row + e));
+                    bl = v > b1 || (v == b1 && l > bl) ? l : bl;
                     if (v > b1) { b2 = b1; b1 = v; }
                     else if (v > b2) b2 = v;
                 }
@@ -192,12 +199,14 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
                 const double m2 = warp_max_d(lane == who ? b2 : b1);
                 v = m2 > -INFINITY ? m1 + m2 : m1;
             }
-            if (lane == g) mine = v;
+            const float ml = scored_groups ? 0.0f : warp_max1(b1 == m1 ? bl : -INFINITY);
+            if (lane == g) { mine = v; minel = ml; }
         }
         int rank = 0;
         for (int g = 0; g < a.G; ++g) {
             const double v = __shfl_sync(0xffffffffu, mine, g);
-            rank += (v > mine || (v == mine && g < lane)) ? 1 : 0;
+            const float l = __shfl_sync(0xffffffffu, minel, g);
+            rank += (v > mine || (v == mine && (l > minel || (l == minel && g < lane)))) ? 1 : 0;
         }
         const unsigned kept = __ballot_sync(0xffffffffu, lane < a.G && rank < a.keep);
 #pragma unroll 1
@@ -212,13 +221,21 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
     int my_id = 0;
     bool my_on = false;
     for (int j = 0; j < a.k; ++j) {
+        // the largest key, of those the largest logit (slots that are off: none), of
+        // those the lowest expert
         double best = -INFINITY;
+        float bl = -INFINITY;
         int slot = -1;
 #pragma unroll 1
         for (int i = 0; i < SLOTS; ++i)
-            if (((live >> i) & 1u) && (slot < 0 || key[i] > best)) { best = key[i]; slot = i; }
+            if ((live >> i) & 1u) {
+                const float l = key[i] > -INFINITY ? sel_cap(__ldg(row + lane + 32 * i)) : -INFINITY;
+                if (slot < 0 || key[i] > best || (key[i] == best && l > bl)) { best = key[i]; bl = l; slot = i; }
+            }
         const double m = warp_max_d(slot >= 0 ? best : -INFINITY);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, slot >= 0 && best == m ? (uint32_t)(lane + 32 * slot) : 0xffffffffu);
+        const bool top_key = slot >= 0 && best == m;
+        const float ml = warp_max1(top_key ? bl : -INFINITY);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, top_key && bl == ml ? (uint32_t)(lane + 32 * slot) : 0xffffffffu);
         if ((int)(e & 31u) == lane) live &= ~(1u << (e >> 5));
         if (lane == j) { my_id = (int)e; my_on = m > -INFINITY; }
     }
@@ -250,30 +267,49 @@ struct __align__(16) SelScratch {
     double exact[kSelCand];              // fp64 keys, where they are needed
 };
 
-// The candidates ranked by their keys in fp64
+// The candidates ranked by their keys in fp64, then by their logits
 __device__ __noinline__ void rank_exact(const SelectArgs& a, const float* row, float top, int C, SelScratch& sc) {
     const int lane = threadIdx.x & 31;
     const double total = softmax_total(a, row, top);
     double mine[2] = {0.0, 0.0};
-    int e[2] = {0, 0}, rank[2] = {0, 0};
+    int rank[2] = {0, 0};
 #pragma unroll 1
     for (int u = 0; u < 2; ++u) {
         const int j = lane + 32 * u;
         if (j < C) {
-            e[u] = sc.expert[j];
-            mine[u] = exact_score(a, (double)sel_cap(__ldg(row + e[u])), top, total) + (double)sel_cap(__ldg(a.bias + e[u]));
+            const int e = sc.expert[j];
+            const float l = sel_cap(__ldg(row + e));
+            mine[u] = exact_score(a, (double)l, top, total) + (double)sel_cap(__ldg(a.bias + e));
             sc.exact[j] = mine[u];
+            sc.key[j] = sel_key(l);                  // (the fp32 keys have done their work)
         }
     }
     __syncwarp();
     for (int j = 0; j < C; ++j) {
         const double v = sc.exact[j];
-        const int o = sc.expert[j];
-        for (int u = 0; u < 2; ++u) rank[u] += (v > mine[u] || (v == mine[u] && o < e[u])) ? 1 : 0;
+        for (int u = 0; u < 2; ++u) rank[u] += v > mine[u] ? 1 : 0;
     }
-    for (int u = 0; u < 2; ++u)
-        if (lane + 32 * u < C) sc.order[rank[u]] = lane + 32 * u;
+    auto place = [&] {
+        for (int u = 0; u < 2; ++u)
+            if (lane + 32 * u < C) sc.order[rank[u]] = lane + 32 * u;
+        __syncwarp();
+    };
+    place();
+    // equal keys meet at one rank, and one of them does not find itself there
+    bool met = false;
+    for (int u = 0; u < 2; ++u) met = met || (lane + 32 * u < C && sc.order[rank[u]] != lane + 32 * u);
+    if (!__any_sync(0xffffffffu, met)) return;
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        if (i >= C) continue;
+        const uint32_t li = sc.key[i];
+        const int e = sc.expert[i];
+        for (int j = 0; j < C; ++j)
+            rank[u] += sc.exact[j] == mine[u] && (sc.key[j] > li || (sc.key[j] == li && sc.expert[j] < e)) ? 1 : 0;
+    }
     __syncwarp();
+    place();
 }
 
 // The candidates ranked by fp32 key, the lower expert first on equal keys.
@@ -348,13 +384,19 @@ __device__ __noinline__ int group_rank_exact(const SelectArgs& a, const float* r
         if (hit) { sc.expert[p] = e; sc.order[p] = g; }
     }
     __syncwarp();
-    for (int j = lane; j < n; j += 32)
-        sc.exact[j] = exact_score(a, (double)sel_cap(__ldg(row + sc.expert[j])), top, total) + (a.bias ? (double)sel_cap(__ldg(a.bias + sc.expert[j])) : 0.0);
+    for (int j = lane; j < n; j += 32) {
+        const float l = sel_cap(__ldg(row + sc.expert[j]));
+        sc.exact[j] = exact_score(a, (double)l, top, total) + (a.bias ? (double)sel_cap(__ldg(a.bias + sc.expert[j])) : 0.0);
+        sc.key[j] = top2 ? 1u : sel_key(l);          // decides between equal scores that are single keys
+    }
     __syncwarp();
     double d1 = -INFINITY, d2 = -INFINITY;
+    uint32_t dl = 0u;                                // the largest key's logit
     for (int j = 0; j < n; ++j)
         if (sc.order[j] == g) {
             const double x = sc.exact[j];
+            const uint32_t l = sc.key[j];
+            dl = x > d1 || (x == d1 && l > dl) ? l : dl;
             d2 = fmax(d2, fmin(d1, x));
             d1 = fmax(d1, x);
         }
@@ -363,7 +405,8 @@ __device__ __noinline__ int group_rank_exact(const SelectArgs& a, const float* r
     int rank = 0;
     for (int q = 0; q < a.G; ++q) {
         const double x = __shfl_sync(all, mine, q << gl);
-        rank += (x > mine || (x == mine && q < g)) ? 1 : 0;
+        const uint32_t l = __shfl_sync(all, dl, q << gl);
+        rank += (x > mine || (x == mine && (l > dl || (l == dl && q < g)))) ? 1 : 0;
     }
     return rank;
 }

@@ -320,15 +320,17 @@ moe_status moe_set_expert_table(moe_handle h, const void* const* blocks, moe_str
  *           part in it, not even one that is off), or 1 / (1 + exp(-l_e))
  *   key_e = s_e + bias_e; without a bias the keys' order is the logits' order
  *   groups of E / num_groups consecutive experts; the top_groups best by
- *           group_score stay (the lower group on ties, groups without an
- *           eligible expert last)
- *   ids   = the k best keys of the groups that stay, key descending, expert
- *           ascending on equal keys; slots that find no eligible expert take
+ *           group_score stay (groups without an eligible expert last)
+ *   ids   = the k best keys of the groups that stay, key descending; slots that
+ *           find no eligible expert take
  *           the lowest-numbered experts not chosen, with weight 0, so that the
  *           ids stay distinct and valid for moe_forward (a fully masked token
  *           gets experts 0 .. k-1 and weights 0)
  *   w_j   = scale * s_j, divided by the sum of the chosen s when renorm is set
- * The order is that of the exact keys, not of their fp32 roundings. */
+ * Keys and group scores are compared in 64 bits, not in their fp32 roundings.
+ * Where two are equal there, the larger logit goes first (for groups by
+ * MOE_GROUP_MAX, that of the largest key; scores rise with their logits), then
+ * the lower expert or group. */
 typedef struct {
     int32_t score;             /* MOE_SCORE_* */
     int32_t num_groups;        /* 1 (no groups) .. 32, dividing E */

@@ -528,7 +528,9 @@ def select_experts(logits, k, score="softmax", bias=None, num_groups=1, top_grou
     """Expert ids [T, k] and fp64 weights of fp32 logits [T, E] under a routing
     rule.  NaN, -inf and the lowest finite fp32 value switch an expert off (as
     a logit altogether, as a bias for the selection alone: its score stays in the
-    softmax's sum); +inf counts as the largest finite value."""
+    softmax's sum); +inf counts as the largest finite value.  Keys that are equal
+    in fp64 go by their logits (scores rise with them), then by number; groups by
+    the logit of their largest key, where that key is their score."""
     logits = np.asarray(logits, dtype=np.float64)
     T, E = logits.shape
     ids = np.zeros((T, k), dtype=np.int32)
@@ -548,17 +550,18 @@ def select_experts(logits, k, score="softmax", bias=None, num_groups=1, top_grou
             on = [e for e in on if float(bias[e]) > -F32_MAX]
         key = {e: (x[e] if bias is None else s[e] + min(float(bias[e]), F32_MAX)) for e in on}
         if num_groups > 1:
-            value = {}
+            value, tie = {}, {}
             for g in range(num_groups):
                 mine = [e for e in on if e // per == g]
+                tie[g] = 0.0
                 if group_score == "top2" and per > 1:
                     v = sorted(((s[e] if bias is None else key[e]) for e in mine), reverse=True)[:2]
                     value[g] = sum(v) if v else -np.inf
                 else:
-                    value[g] = max((key[e] for e in mine), default=-np.inf)
-            kept = sorted(range(num_groups), key=lambda g: (-value[g], g))[:top_groups]
+                    value[g], tie[g] = max(((key[e], x[e]) for e in mine), default=(-np.inf, 0.0))
+            kept = sorted(range(num_groups), key=lambda g: (-value[g], -tie[g], g))[:top_groups]
             on = [e for e in on if e // per in kept]
-        chosen = sorted(on, key=lambda e: (-key[e], e))[:k]
+        chosen = sorted(on, key=lambda e: (-key[e], -x[e], e))[:k]
         rest = [e for e in range(E) if e not in chosen][: k - len(chosen)]
         ids[t] = chosen + rest
         if not chosen:

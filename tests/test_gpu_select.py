@@ -105,6 +105,25 @@ def test_masks(score, G, renorm):
             check(L, k, b, score=score, num_groups=G, top_groups=max(1, G // 2), group_score=gs, renorm=renorm)
 
 
+@pytest.mark.parametrize("score,shift,spread", [("sigmoid", 45.0, 3.0), ("sigmoid", 120.0, 30.0), ("sigmoid", -900.0, 60.0), ("softmax", 0.0, 400.0)])
+@pytest.mark.parametrize("E,G,keep", [(40, 1, 1), (512, 1, 1), (512, 8, 3), (1000, 5, 2)])
+@pytest.mark.parametrize("level", [0.0, 0.75])
+def test_a_bias_of_one_value_changes_no_order(score, shift, spread, E, G, keep, level):
+    """Saturated and vanished scores, whose keys are equal in 64 bits: their logits
+    say which is larger, as without a bias (up to 1000 of them, more than a list
+    holds, and a few among others)."""
+    k = 8
+    rng = np.random.default_rng(E + G)
+    L = (shift + spread * rng.standard_normal((10, E))).astype(np.float32)
+    if score == "sigmoid" and shift > 0:
+        L[5:, 9:] -= shift + 30.0
+    bias = np.full(E, level, dtype=np.float32)
+    check(L, k, bias, score=score, num_groups=G, top_groups=keep)
+    want, _ = run(L, k, score=score, num_groups=G, top_groups=keep)
+    got, _ = run(L, k, bias, score=score, num_groups=G, top_groups=keep)
+    assert np.array_equal(got, want)
+
+
 @pytest.mark.parametrize("E,G,keep", [(48, 1, 1), (48, 4, 2), (600, 24, 5), (1024, 1, 1)])
 @pytest.mark.parametrize("group_score", ["max", "top2"])
 def test_a_bias_that_is_off_changes_no_score(E, G, keep, group_score):

@@ -44,6 +44,18 @@ def test_selection_masks():
     assert w.tolist() == [[1.0, 0.0], [0.0, 0.0], [0.5, 0.5]]
 
 
+def test_keys_that_are_equal_in_64_bits_go_by_their_logits():
+    """Scores that saturate, or vanish beside their biases: a bias of one value
+    changes no order."""
+    L = np.array([[40.0, 50.0, 45.0, 50.0], [-800.0, -900.0, -850.0, 0.0]], dtype=np.float32)
+    for bias in (None, np.zeros(4, dtype=np.float32), np.full(4, 3.0, dtype=np.float32)):
+        assert O.select_experts(L, 3, score="sigmoid", bias=bias)[0].tolist() == [[1, 3, 2], [3, 0, 2]]
+        assert O.select_experts(L, 1, score="sigmoid", bias=bias, num_groups=2)[0].tolist() == [[1], [3]]
+        assert O.select_experts(L[:1, [2, 0, 1, 0]], 1, score="sigmoid", bias=bias, num_groups=2)[0].tolist() == [[2]]
+    for bias in (None, np.zeros(4, dtype=np.float32)):
+        assert O.select_experts(L, 3, bias=bias)[0].tolist() == [[1, 3, 2], [3, 0, 2]]
+
+
 def test_a_bias_takes_no_part_in_the_scores():
     """Softmax scores 1/2, 1/4, 1/4; a bias that switches expert 0 off leaves the
     others theirs."""
