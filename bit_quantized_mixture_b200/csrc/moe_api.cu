@@ -920,6 +920,17 @@ static bool rows_overlap(const void* p, int64_t lp, int64_t wp, const void* q, i
     return d < wp || d + wq > lp;
 }
 
+// Do rows p[T][wp] (lp apart, in bytes) and the n bytes at q share a byte?  (q between
+// two rows does not)
+static bool rows_meet(const void* p, int64_t lp, int64_t wp, int64_t T, const void* q, int64_t n) {
+    if (!p || !q) return false;
+    const int64_t a = (int64_t)(uintptr_t)p, b = (int64_t)(uintptr_t)q;
+    if (b >= a + (T - 1) * lp + wp || a - b >= n) return false;
+    if (b <= a || T == 1) return true;
+    const int64_t row = (b - a) / lp, in = (b - a) % lp;     // the last row that starts at or before q
+    return in < wp || (row + 1 < T && lp - in < n);
+}
+
 // Tokens of a call without a handle, and columns: row, tile and column numbers stay below 2^31
 constexpr int32_t kMaxRows = 1 << 30;
 
@@ -1093,6 +1104,11 @@ static moe_status check_norm(moe_layer* h, const char* fn, const moe_norm* n) {
     auto same = [&](const Rows& a, const Rows& b) { return a.p == b.p && (a.ld == b.ld || T == 1); };
     if ((!same(ro, r) && clash(ro, r)) || (!same(xo, y) && clash(xo, y)) || clash(ro, y) || clash(xo, r) || clash(ro, xo) ||
         clash(ro, g) || clash(xo, g))
+        return fail(h, MOE_ERR_INVALID_ARG, "%s: an output overlaps another tensor", fn);
+    // the vectors that every row reads
+    auto meets = [&](const void* q, int64_t bytes) { return rows_meet(ro.p, ro.ld, ro.w, T, q, bytes) || rows_meet(xo.p, xo.ld, xo.w, T, q, bytes); };
+    if (meets(n->w_post, w2) || meets(n->w_pre, w2) || (n->gate_kind == MOE_GATE_CHANNEL && meets(n->gate, w2)) ||
+        (n->gate_kind == MOE_GATE_TOKEN && meets(n->gate, (int64_t)T * 4)))
         return fail(h, MOE_ERR_INVALID_ARG, "%s: an output overlaps another tensor", fn);
     return MOE_OK;
 }

@@ -154,3 +154,18 @@ def test_no_tokens_and_refusals():
                dict(r_out=torch.empty(4, 64, device=DEV)), dict(y=None), dict(gate=d["gate"].cpu())):
         with pytest.raises(moe.MoeError):
             moe.block_norm(**{**d, **kw})
+
+
+def test_vectors_between_an_outputs_rows():
+    """A weight that lies between two rows of an output overlaps nothing."""
+    T, H = 6, 512
+    d = make(T, H, False, True, "channel", True, seed=4)
+    want = moe.block_norm(**d)
+    big = torch.zeros(T, 2 * H, dtype=torch.bfloat16, device=DEV)
+    for row, name in ((0, "post_weight"), (3, "pre_weight"), (5, "gate")):
+        big[row, H:] = d[name]
+        d[name] = big[row, H:]
+    got = moe.block_norm(**d, x_out=big[:, :H])
+    assert torch.equal(got[0], want[0]) and torch.equal(big[:, :H], want[1]) and torch.equal(big[3, H:], d["pre_weight"])
+    with pytest.raises(moe.MoeError):
+        moe.block_norm(**{**d, "pre_weight": big[2, 8:8 + H]}, x_out=big[:, :H])

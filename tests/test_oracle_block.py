@@ -202,6 +202,16 @@ def test_norm_refusals(kw, status, text):
     assert st == status and text in _err()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(w_post=BASE + 128), dict(w_post=BASE + 8192 + 256), dict(w_pre=BASE + 384), dict(w_pre=BASE + 8192 - 16),
+    dict(gate_kind=1, gate=BASE + 64), dict(gate_kind=1, gate=BASE + 8192), dict(gate_kind=2, gate=BASE + 508), dict(gate_kind=2, gate=BASE + 8192 - 12),
+    dict(ld_x=128, w_pre=BASE + 8192 + 256 + 64), dict(ld_x=128, w_pre=BASE + 8192 + 128 + 16)])
+def test_norm_refuses_outputs_over_what_every_row_reads(kw):
+    """r_out is 512 bytes at BASE, x_out 512 at BASE + 8192 (896 with rows 256 apart)."""
+    far = dict(w_post=BASE + 16384, w_pre=BASE + 16640)
+    assert moe.lib().moe_block_norm(_norm(**{**far, **kw}), None) == 1 and "overlaps" in _err()
+
+
 def test_addresses_and_sizes_out_of_range():
     """Row distances whose addresses would pass 64 bits, tokens past 2^30, misaligned 4-byte tensors, and
     selections written over what they read."""
