@@ -1022,6 +1022,12 @@ static moe_status check_adapters(moe_layer* h, const char* fn, const moe_adapter
     return MOE_OK;
 }
 
+// bytes of n bf16 matrices of r x c (at most 2^60: beyond any address)
+static int64_t stack_bytes(int64_t n, int64_t r, int64_t c) {
+    const double b = 2.0 * (double)n * (double)r * (double)c;
+    return b < 0x1p60 ? 2 * n * r * c : (int64_t)1 << 60;
+}
+
 static AdapterArgs adapter_args(const void* x, int64_t ld_x, const void* y, int64_t ld_y, void* out, int64_t ld_out,
                                 int32_t wide, int32_t T, const int32_t* ids, const moe_adapters* ad, int* err = nullptr) {
     AdapterArgs a{};
@@ -1052,6 +1058,11 @@ moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t 
     const int64_t wx = (int64_t)ad->K * 2, wy = (int64_t)ad->N * es, lo = row_bytes(ld_out, es, T);
     if (rows_overlap(x, row_bytes(ld_x, 2, T), wx, out, lo, wy, T) ||
         (!in_place && rows_overlap(y, row_bytes(ld_y, es, T), wy, out, lo, wy, T)))
+        return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
+    auto meets = [&](const void* q, int64_t bytes) { return rows_meet(out, lo, wy, T, q, bytes); };
+    const int64_t n = ad->num_adapters;
+    if (meets(adapter_ids, (int64_t)T * 4) || meets(ad->scales, n * 4) || meets(ad->ranks, n * 4) || meets(ad->a, stack_bytes(n, ad->R, ad->K)) ||
+        meets(ad->b, stack_bytes(n, ad->R, ad->N)))
         return fail(nullptr, MOE_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
     const cudaError_t e = launch_add_adapters(adapter_args(x, ld_x, y, ld_y, out, ld_out, y_fp32, T, adapter_ids, ad),
                                               (cudaStream_t)stream);

@@ -202,6 +202,16 @@ def test_norm_refusals(kw, status, text):
     assert st == status and text in _err()
 
 
+@pytest.mark.parametrize("ad,ids", [
+    (dict(a=BASE + 8192 + 496), BASE), (dict(a=BASE + 8192 - 4096 + 16), BASE), (dict(b=BASE + 8192), BASE), (dict(scales=BASE + 8192 + 508), BASE),
+    (dict(ranks=BASE + 8192 - 4), BASE), ({}, BASE + 8192 + 256), (dict(num_adapters=0x7fffffff, R=128, K=64), BASE)])
+def test_adapters_refuse_outputs_over_their_inputs(ad, ids):
+    """out, 512 bytes at BASE + 8192, over the adapters (the last: 2^45 bytes from BASE
+    on), their scales and ranks, the ids."""
+    st = moe.lib().moe_add_adapters(BASE, 64, BASE + 16384, 64, BASE + 8192, 64, 0, 4, ids, _adapters(**ad), None)
+    assert st == 1 and "overlaps" in _err()
+
+
 @pytest.mark.parametrize("kw", [
     dict(w_post=BASE + 128), dict(w_post=BASE + 8192 + 256), dict(w_pre=BASE + 384), dict(w_pre=BASE + 8192 - 16),
     dict(gate_kind=1, gate=BASE + 64), dict(gate_kind=1, gate=BASE + 8192), dict(gate_kind=2, gate=BASE + 508), dict(gate_kind=2, gate=BASE + 8192 - 12),
