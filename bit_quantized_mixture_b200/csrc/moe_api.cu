@@ -1171,6 +1171,32 @@ moe_status moe_block_forward(moe_handle h, const moe_block* b, moe_stream_t stre
     }
     if (b->router_adapters && b->logits && !aligned16(b->logits))
         return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: logits must be 16-byte aligned");
+    if (!aligned4(b->logits) || !aligned4(b->topk_ids) || !aligned4(b->topk_w) || !aligned4(b->adapter_ids))
+        return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: logits, ids, weights and adapter ids must be 4-byte aligned");
+    // What a step writes lies over no other result and over nothing that is given
+    // (r against x, y and x_next, and x_next against y: above, and by check_norm; x_next
+    // may be x, which nothing reads any more; the gate may be one of the results).
+    struct Span { const void* p; int64_t n; };
+    const Span out[] = {{b->x, T * w2}, {b->y, T * w2}, {b->topk_ids, (int64_t)T * c.top_k * 4}, {b->topk_w, (int64_t)T * c.top_k * 4},
+                        {b->logits, (int64_t)T * c.num_experts * 4}, {b->x_next, T * w2}};
+    constexpr int kOut = sizeof out / sizeof out[0];
+    auto meet = [](const Span& p, const Span& q) { return p.p && q.p && spans_meet(p.p, p.n, q.p, q.n); };
+    for (int i = 0; i < kOut; ++i)
+        for (int j = i + 1; j < kOut; ++j)
+            if (!(i <= 1 && j == kOut - 1) && meet(out[i], out[j]))
+                return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: two results overlap");
+    Span given[13] = {{b->r, T * wr}, {b->w_in, w2}, {b->w_post, w2}, {b->w_next, w2}, {b->adapter_ids, (int64_t)T * 4}};
+    for (int i = 0; i < 2; ++i)
+        if (const moe_adapters* ad = ads[i]) {
+            Span* g = given + 5 + 4 * i;
+            g[0] = {ad->a, stack_bytes(ad->num_adapters, ad->R, ad->K)};
+            g[1] = {ad->b, stack_bytes(ad->num_adapters, ad->R, ad->N)};
+            g[2] = {ad->scales, (int64_t)ad->num_adapters * 4};
+            g[3] = {ad->ranks, (int64_t)ad->num_adapters * 4};
+        }
+    for (const Span& g : given)
+        for (int i = b->w_in ? 0 : 1; i < kOut; ++i)             // (without w_in x is given, too)
+            if (meet(g, out[i])) return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: a result overlaps an input");
     moe_norm n{};
     n.r = b->r; n.T = T; n.H = H; n.r_fp32 = b->r_fp32;
     n.ld_r = n.ld_y = n.ld_gate = n.ld_r_out = n.ld_x = H;

@@ -426,7 +426,9 @@ moe_status moe_block_norm(const moe_norm* norm, moe_stream_t stream);
  *   logits = x Wr^T (+ router_adapters), selection, y = moe_forward(x)
  *   y += layer_adapters                    (K = N = H)
  *   r, x_next = moe_block_norm(r, y)
- * r is updated in place.  Rows are contiguous (ld = H). */
+ * r is updated in place.  Rows are contiguous (ld = H).  Results overlap neither
+ * one another nor what is given, but that x_next may be y or x; the gate may be
+ * one of the results. */
 typedef struct {
     void* r;                   /* bf16 or (r_fp32) fp32 [T, H], in and out */
     void* x;                   /* bf16 [T, H]: out with w_in, else in */
