@@ -103,7 +103,7 @@ MOE_DEV void st_cluster_v4(void* p, int rank, uint4 v) {
 MOE_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 MOE_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // bounded wait that acquires what the cluster's arrivals released
-MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code, long long limit) {
     const long long t0 = clock64();
     while (true) {
         uint32_t ok;
@@ -111,15 +111,15 @@ MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abo
                      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
         if (ok) return true;
         if (*abort_flag) return false;
-        if (clock64() - t0 > kWaitLimitCycles) {
+        if (clock64() - t0 > limit) {
             *abort_flag = 1;
             if (err) atomicCAS(err, 0, code);
             return false;
         }
     }
 }
-MOE_DEV bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
+MOE_DEV bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code, long long limit) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code, limit));
 }
 // 16-byte piece j of row r of a 128-byte-swizzled tile
 MOE_DEV uint32_t sw_piece(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
@@ -147,8 +147,14 @@ MOE_DEV void wait_some(uint64_t* bar, uint32_t parity) {
     for (int q = 0; q < 1000 && !mbar_try_wait(bar, parity); ++q) {}
 }
 
-// where a call without an error word of its own records a wait that gave up
-__device__ int g_wait_err;
+// Calls without an error word of their own: how many CTAs have given up a wait on
+// this device, and the last one's site.  It only grows, so that no report is lost to
+// another stream's and every stream can ask for itself.
+struct WaitErrors {
+    unsigned count;
+    int code;
+};
+__device__ WaitErrors g_wait_errors;
 
 // 32 output columns of a row, taken again in fp32 (a NaN among them whose z parts
 // cannot tell, see adapters.cuh; rare, so not inlined).  n: the first column's
@@ -183,17 +189,19 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t big_full[kTcStreams][NBIG], big_empty[kTcStreams][NBIG], chunk_done[kTcStreams][NBIG];
     __shared__ uint64_t small_full[kTcStreams][NSMALL], small_empty[kTcStreams][NSMALL], small_clean[kTcStreams][NSMALL];
-    __shared__ uint64_t z_full, z_free, z_ready, z_read, op_full;
+    __shared__ uint64_t z_full, z_free, z_ready, z_read, op_full, mma_done[kTcStreams];
     __shared__ uint64_t d_full[kTcStreams][kTcDBufs], d_empty[kTcStreams][kTcDBufs];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, s_err;
+    __shared__ int s_sent[2 * kTcStreams];       // loads of x and y, of A and B by stream
     __shared__ int s_id[kTcRows], s_list[kTcRows], s_rank[kTcRows];
     __shared__ unsigned s_first[4];
     __shared__ float s_scale[kTcRows];
     // the swizzle and its descriptors count from 1024-byte boundaries
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     cg::cluster_group cl = cg::this_cluster();
-    int* const err = a.err ? a.err : &g_wait_err;
+    int* const err = a.err ? a.err : &s_err;
+    const long long limit = a.wait_limit > 0 ? a.wait_limit : kWaitLimitCycles;
     const int CL = (int)cl.num_blocks(), crank = (int)cl.block_rank();
     const int t0 = (int)(blockIdx.x / CL) * kTcRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -252,7 +260,9 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         mbar_init(&z_ready, (uint32_t)(kTcEpiWarps * CL));
         mbar_init(&z_read, (uint32_t)(kTcEpiWarps * CL));
         mbar_init(&op_full, (uint32_t)(kTcEpiWarps * CL));
+        for (int w = 0; w < kTcStreams; ++w) mbar_init(&mma_done[w], 1);
         abort_flag = 0;
+        s_err = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
         Turned kc(k0, k1, turn);
@@ -287,16 +297,18 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         // ------------------------------ producer of x and y (one thread)
         if (lane == 0) {
             Ring<NBIG> ring[kTcStreams];
+            int sent[kTcStreams] = {0, 0};
             bool ok = true;
             auto send = [&](int i, const CUtensorMap* map, int col, bool out) {
                 Ring<NBIG>& r = ring[i & (kTcStreams - 1)];
                 const int w = i & (kTcStreams - 1);
                 if (!out) {
-                    ok = mbar_wait(&big_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 41);
+                    ok = mbar_wait(&big_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 41, limit);
                     if (!ok) return;
                     mbar_arrive_expect_tx(&big_full[w][r.slot], C::BIG);
                     tma_load_2d(smem + (w * NBIG + r.slot) * C::BIG, map, col, t0, &big_full[w][r.slot]);
                 }
+                ++sent[w];
                 r.next();
             };
             for (int p = 0; ok && p < passes; ++p) {
@@ -306,12 +318,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             }
             Turned nc(n0, n1, turn);
             for (int i = 0; ok && i < n1 - n0; ++i, nc.next()) send(i, &maps.y, NC * nc.at, false);
-            if (!ok)                                 // given up: let what is in flight land (bounded)
-                for (int w = 0; w < kTcStreams; ++w)
-                    // the slots before the current one in this round of the ring,
-                    // the others in the round before (a slot not used yet in that
-                    // round reads as complete)
-                    for (int i = 0; i < NBIG; ++i) wait_some(&big_full[w][i], i < ring[w].slot ? ring[w].phase : ring[w].phase ^ 1u);
+            for (int w = 0; w < kTcStreams; ++w) s_sent[w] = max(sent[w], count(0, early, w));
         }
         __syncwarp();
     } else if (warp == kTcSmall || warp == kTcSmall + 1) {
@@ -319,6 +326,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         if (lane == 0) {
             const int w = warp - kTcSmall;
             Ring<NSMALL> r;
+            int sent = 0;
             bool ok = true;
             uint8_t* slots = smem + C::OFF_SMALL + w * NSMALL * C::SMALL;
             for (int p = 0; ok && p < passes; ++p) {
@@ -326,8 +334,8 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                 Turned kc(k0, k1, turn);
                 for (int i = 0; ok && i < k1 - k0; ++i, kc.next()) {
                     if ((i & (kTcStreams - 1)) != w) continue;
-                    for (int d = d0; d < d1; ++d, r.next()) {
-                        if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 42))) break;
+                    for (int d = d0; d < d1; ++d, r.next(), ++sent) {
+                        if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 42, limit))) break;
                         mbar_arrive_expect_tx(&small_full[w][r.slot], (uint32_t)rows_a * 128u);
                         tma_load_3d(slots + r.slot * C::SMALL, &maps.a, 64 * kc.at, 0, s_list[d], &small_full[w][r.slot]);
                     }
@@ -336,16 +344,15 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             Turned nc(n0, n1, turn);
             for (int i = 0; ok && i < n1 - n0; ++i, nc.next()) {
                 if ((i & (kTcStreams - 1)) != w) continue;
-                for (int d = 0; d < D; ++d, r.next()) {
-                    if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 44))) break;
+                for (int d = 0; d < D; ++d, r.next(), ++sent) {
+                    if (!(ok = mbar_wait(&small_empty[w][r.slot], r.phase ^ 1u, &abort_flag, err, 44, limit))) break;
                     const int nb = (s_rank[d] + 63) / 64;
                     mbar_arrive_expect_tx(&small_full[w][r.slot], (uint32_t)(nb * NC * 128));
                     for (int b = 0; b < nb; ++b)
                         tma_load_3d(slots + r.slot * C::SMALL + b * NC * 128, &maps.b, 64 * b, NC * nc.at, s_list[d], &small_full[w][r.slot]);
                 }
             }
-            if (!ok)
-                for (int i = 0; i < NSMALL; ++i) wait_some(&small_full[w][i], i < r.slot ? r.phase : r.phase ^ 1u);
+            s_sent[kTcStreams + w] = sent;
         }
         __syncwarp();
     } else if (warp <= kTcStreams) {
@@ -363,13 +370,13 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             const uint32_t idz = idesc_bf16_f32(kTcRows, rows_a), ido = idesc_bf16_f32(kTcRows, NC);
             for (int p = 0; ok && p < passes; ++p) {
                 const int nd = min(D - p * per_pass, per_pass);
-                if (p > 0 && !(ok = mbar_wait(&z_free, (uint32_t)(p - 1) & 1u, &abort_flag, err, 45))) break;
+                if (p > 0 && !(ok = mbar_wait(&z_free, (uint32_t)(p - 1) & 1u, &abort_flag, err, 45, limit))) break;
                 tc_fence_after();
                 for (int kc = k0 + w; ok && kc < k1; kc += kTcStreams, big.next()) {
-                    if (!(ok = mbar_wait(&big_full[w][big.slot], big.phase, &abort_flag, err, 46))) break;
+                    if (!(ok = mbar_wait(&big_full[w][big.slot], big.phase, &abort_flag, err, 46, limit))) break;
                     const uint64_t xd = dx + (uint64_t)(big.slot * (C::BIG >> 4));
                     for (int d = 0; d < nd; ++d, small.next()) {
-                        if (!(ok = mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, err, 47))) break;
+                        if (!(ok = mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, err, 47, limit))) break;
                         const uint64_t ad = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
                         const uint32_t dst = tmem + (uint32_t)((d * kTcStreams + w) * rows_a);
 #pragma unroll
@@ -381,15 +388,15 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                 if (ok && w < k1 - k0) mma_commit(&z_full);
             }
             if (ok && D > 0) {
-                ok = mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 48);
+                ok = mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 48, limit);
                 fence_proxy_async_smem();            // the operand came by ordinary stores
             }
             for (int nc = n0 + w; ok && nc < n1; nc += kTcStreams)
                 for (int d = 0; d < D; ++d, small.next(), ++unit) {
                     const int buf = unit & 1, steps = (s_rank[d] + 15) / 16;
-                    ok = a.ranks ? mbar_wait(&small_clean[w][small.slot], (uint32_t)(unit / NSMALL) & 1u, &abort_flag, err, 49)
-                                 : mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, err, 49);
-                    ok = ok && mbar_wait(&d_empty[w][buf], ((uint32_t)(unit >> 1) & 1u) ^ 1u, &abort_flag, err, 50);
+                    ok = a.ranks ? mbar_wait(&small_clean[w][small.slot], (uint32_t)(unit / NSMALL) & 1u, &abort_flag, err, 49, limit)
+                                 : mbar_wait(&small_full[w][small.slot], small.phase, &abort_flag, err, 49, limit);
+                    ok = ok && mbar_wait(&d_empty[w][buf], ((uint32_t)(unit >> 1) & 1u) ^ 1u, &abort_flag, err, 50, limit);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t bd = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
@@ -406,6 +413,8 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                     mma_commit(&small_empty[w][small.slot]);
                     mma_commit(&d_full[w][buf]);
                 }
+            mma_commit(&mma_done[w]);                // nothing of this thread's runs on when the CTA ends
+            wait_some(&mma_done[w], 0u);
         }
         __syncwarp();
     } else if (warp == kTcStore) {
@@ -418,7 +427,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             bool ok = true;
             for (int i = 0; ok && i < n1 - n0; ++i, at.next()) {
                 const int w = i & (kTcStreams - 1), s = ring[w].slot;
-                if (!(ok = mbar_wait(&chunk_done[w][s], ring[w].phase, &abort_flag, err, 59))) break;
+                if (!(ok = mbar_wait(&chunk_done[w][s], ring[w].phase, &abort_flag, err, 59, limit))) break;
                 tma_store_2d(&maps.out, NC * at.at, t0, smem + (w * NBIG + s) * C::BIG);
                 bulk_commit();
                 bulk_wait_read<0>();
@@ -439,13 +448,13 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         if (a.ranks) {
             // the first product's uses of the slots are over then, and the slots
             // go on where it left off
-            bool ok = D == 0 || __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 57));
+            bool ok = D == 0 || __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 57, limit));
             const int w = warp == kTcCleaner ? 0 : 1;
             int used = D * count(k0, k1, w);
             for (int nc = n0 + w; ok && nc < n1; nc += kTcStreams) {
                 for (int d = 0; d < D; ++d, ++used) {
                     const int slot = used % NSMALL;
-                    if (!(ok = all_wait(&small_full[w][slot], (uint32_t)(used / NSMALL) & 1u, &abort_flag, err, 56))) break;
+                    if (!(ok = all_wait(&small_full[w][slot], (uint32_t)(used / NSMALL) & 1u, &abort_flag, err, 56, limit))) break;
                     const int rank = s_rank[d], steps = (rank + 15) / 16;
                     if (rank & 15) {
                         uint8_t* bt = smem + C::OFF_SMALL + (w * NSMALL + slot) * C::SMALL;
@@ -487,7 +496,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             const int own_rows = kTcRows / CL, owner = row / own_rows, quads = rows_a / 4;
             float4* zp = reinterpret_cast<float4*>(smem + C::OFF_Z);
             for (int p = 0; ok && p < passes; ++p) {
-                if (!(ok = all_wait(&z_full, (uint32_t)p & 1u, &abort_flag, err, 51))) break;
+                if (!(ok = all_wait(&z_full, (uint32_t)p & 1u, &abort_flag, err, 51, limit))) break;
                 tc_fence_after();
                 const int nd = min(D - p * per_pass, per_pass);
                 for (int d = 0; d < nd; ++d) {
@@ -518,8 +527,8 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
             }
             __syncwarp();
             if (ok) {
-                if (lane < CL) mbar_arrive_cluster(&z_ready, lane);
-                ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_ready, 0u, &abort_flag, err, 52));
+                if (lane < CL && !((int)blockIdx.x == a.withhold && warp == 3)) mbar_arrive_cluster(&z_ready, lane);
+                ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_ready, 0u, &abort_flag, err, 52, limit));
             }
             if (ok) {
                 // this CTA's rows, eight columns of one at a time: summed and scaled in
@@ -546,7 +555,7 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                 if (C::OFF_Z + rows_a * kTcRows * 4 > C::OFF_OP) {       // the operand takes their place
                     __syncwarp();
                     if (lane < CL) mbar_arrive_cluster(&z_read, lane);
-                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_read, 0u, &abort_flag, err, 53));
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_read, 0u, &abort_flag, err, 53, limit));
                 }
 #pragma unroll
                 for (int u = 0; u < ITEMS; ++u) {
@@ -571,10 +580,10 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         // The first product's uses of the slots are over (a parity tells only one
         // use from the next), and this group's chunks, every other one, go on
         // where its stream left off.
-        if (D == 0) ok = all_wait(&z_full, 0u, &abort_flag, err, 58);
+        if (D == 0) ok = all_wait(&z_full, 0u, &abort_flag, err, 58, limit);
         bool unsure = false;                 // this row has a z that its parts may not stand for
         if (ok && D > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 60));
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&op_full, 0u, &abort_flag, err, 60, limit));
             for (int j = 0; ok && j < rows_a / 8; ++j) {
                 const uint4 p = *reinterpret_cast<const uint4*>(smem + C::OFF_OP + (j >> 3) * C::ZBLOCK + sw_piece(row, j & 7));
                 const uint32_t w[4] = {p.x, p.y, p.z, p.w};
@@ -587,11 +596,11 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
         if (group) at.next();
         for (int nc = n0 + group; ok && nc < n1; nc += kTcStreams, ++big, at.next(), at.next()) {
             const int s = big % NBIG;
-            if (!(ok = all_wait(&big_full[group][s], (uint32_t)(big / NBIG) & 1u, &abort_flag, err, 54))) break;
+            if (!(ok = all_wait(&big_full[group][s], (uint32_t)(big / NBIG) & 1u, &abort_flag, err, 54, limit))) break;
             uint8_t* tile = smem + (group * NBIG + s) * C::BIG;
             for (int d = 0; d < D; ++d, ++unit) {
                 const int buf = unit & 1;
-                if (!(ok = all_wait(&d_full[group][buf], (uint32_t)(unit >> 1) & 1u, &abort_flag, err, 55))) break;
+                if (!(ok = all_wait(&d_full[group][buf], (uint32_t)(unit >> 1) & 1u, &abort_flag, err, 55, limit))) break;
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, mine == d)) {
                     const uint32_t src = tmem + lane_base + kTcZCols + 64u * (uint32_t)(group * kTcDBufs + buf);
@@ -636,6 +645,21 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (abort_flag && threadIdx.x == 0) {
+        // given up: what is in flight lands first (bounded).  A slot of n loads has
+        // had n - 1 whole phases before the last one's.
+        for (int w = 0; w < kTcStreams; ++w) {
+            for (int i = 0; i < NBIG; ++i)
+                if (s_sent[w] > i) wait_some(&big_full[w][i], (uint32_t)((s_sent[w] - i - 1) / NBIG) & 1u);
+            for (int i = 0; i < NSMALL; ++i)
+                if (s_sent[kTcStreams + w] > i) wait_some(&small_full[w][i], (uint32_t)((s_sent[kTcStreams + w] - i - 1) / NSMALL) & 1u);
+        }
+        if (s_err) {
+            atomicExch(&g_wait_errors.code, s_err);
+            __threadfence();
+            atomicAdd(&g_wait_errors.count, 1u);
+        }
+    }
     if (warp == kTcCleaner) tmem_dealloc(tmem, kTcTmemCols);
     if (warp <= kTcStreams || warp >= kTcSmall) cluster_wait();     // of the first arrival
     cluster_arrive();                        // nobody leaves while others may write to its shared memory
@@ -719,14 +743,28 @@ cudaError_t launch_tc(const AdapterArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t take_wait_error(int* code) {
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_wait_err, sizeof(int));
-    const int zero = 0;
-    if (e == cudaSuccess && *code) e = cudaMemcpyToSymbol(g_wait_err, &zero, sizeof(int));
+cudaError_t read_wait_errors(unsigned* count, int* code, cudaStream_t st) {
+    WaitErrors w{};
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&w, g_wait_errors, sizeof w, 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    *count = w.count;
+    *code = w.code;
     return e;
 }
 
-cudaError_t launch_add_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
+// the next launch's test of the bounded waits, on this host thread
+static thread_local int t_withhold = -1;
+static thread_local long long t_wait_limit = 0;
+void set_adapter_wait_test(int withhold, long long limit) {
+    t_withhold = withhold;
+    t_wait_limit = withhold < 0 ? 0 : limit;
+}
+
+cudaError_t launch_add_adapters_tc(const AdapterArgs& args, cudaStream_t st) {
+    AdapterArgs a = args;
+    a.withhold = t_withhold;
+    a.wait_limit = t_wait_limit;
+    set_adapter_wait_test(-1, 0);
     if (a.R <= 64) return a.wide ? launch_tc<1, true>(a, st) : launch_tc<1, false>(a, st);
     // ranks above 64 with fp32 outputs have no variant here
     return a.wide ? cudaErrorNotSupported : launch_tc<2, false>(a, st);

@@ -83,12 +83,18 @@ struct AdapterArgs {
     int T, K, N, R, n;
     bool wide;              // y and out are fp32
     int* err;               // device error word (bounded waits) or null
+    // set by launch_add_adapters_tc: the CTA that withholds an arrival (-1: none) and
+    // the limit of all waits in SM cycles (0: the usual one)
+    int withhold;
+    long long wait_limit;
 };
 // adapters_tc.cu: tiles of 128 tokens on the tensor cores (cudaErrorNotSupported:
 // a tensor that no tensor map describes)
 cudaError_t launch_add_adapters_tc(const AdapterArgs& a, cudaStream_t st);
-// the code of a bounded wait that gave up in a call without an error word (0: none), and clears it
-cudaError_t take_wait_error(int* code);
+// how many CTAs of calls without an error word have given up a bounded wait on the current device so far, and
+// the last one's site, as of what the stream has done; waits for the stream
+cudaError_t read_wait_errors(unsigned* count, int* code, cudaStream_t st);
+void set_adapter_wait_test(int withhold, long long limit);
 cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st);
 
 // block_norm.cu

@@ -7,7 +7,10 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <map>
+#include <mutex>
 #include <new>
+#include <utility>
 
 #include "../../include/moe_b200.h"
 #include "kernels.h"
@@ -1071,11 +1074,24 @@ moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t 
 }
 
 moe_status moe_adapters_status(moe_stream_t stream) {
-    cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
-    int code = 0;
-    if (e == cudaSuccess) e = take_wait_error(&code);
+    int device = 0, code = 0;
+    unsigned count = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = read_wait_errors(&count, &code, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(nullptr, e, "moe_adapters_status");
-    if (code) return fail(nullptr, MOE_ERR_TIMEOUT, "moe_add_adapters gave up a bounded wait (site %d); its outputs are invalid", code);
+    // the device's count only grows; what each stream has been told of it
+    static std::mutex lock;
+    static std::map<std::pair<int, void*>, unsigned> told;
+    std::lock_guard<std::mutex> hold(lock);
+    unsigned& seen = told[{device, stream}];
+    if (count == seen) return MOE_OK;
+    seen = count;
+    return fail(nullptr, MOE_ERR_TIMEOUT, "moe_add_adapters gave up a bounded wait (site %d); its outputs are invalid", code);
+}
+
+moe_status moe_debug_set_adapter_wait_test(int32_t withhold_cta, int64_t wait_limit_cycles) {
+    if (wait_limit_cycles < 0) return fail(nullptr, MOE_ERR_INVALID_ARG, "moe_debug_set_adapter_wait_test: negative limit");
+    set_adapter_wait_test(withhold_cta, wait_limit_cycles);
     return MOE_OK;
 }
 

@@ -34,17 +34,17 @@ MOE_DEV bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Bounded wait: gives up after ~`limit_cycles` SM clocks, records `code` in
-// the global error word and raises the CTA's abort flag.  Returns false on
+// Bounded wait: gives up after ~`limit` SM clocks, records `code` in the
+// error word and raises the CTA's abort flag.  Returns false on
 // timeout (or when another role of the CTA already aborted).
 constexpr long long kWaitLimitCycles = 4000000000LL;   // about 2 s at 1.9 GHz
-MOE_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+MOE_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code, long long limit = kWaitLimitCycles) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
-        if (clock64() - t0 > kWaitLimitCycles) {
+        if (clock64() - t0 > limit) {
             *abort_flag = 1;
             if (err) atomicCAS(err, 0, code);
             return false;

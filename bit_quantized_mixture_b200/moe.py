@@ -112,6 +112,7 @@ def lib():
             "moe_set_routing": [vp, ctypes.POINTER(RoutingRule), vp],
             "moe_add_adapters": [vp, i64, vp, i64, vp, i64, i32, i32, vp, ctypes.POINTER(AdapterSet), vp],
             "moe_adapters_status": [vp],
+            "moe_debug_set_adapter_wait_test": [i32, i64],
             "moe_block_norm": [ctypes.POINTER(Norm), vp],
             "moe_block_forward": [vp, ctypes.POINTER(Block), vp],
             "moe_mma_peak_loop": [i32, i32, i64, vp, ctypes.POINTER(ctypes.c_double), vp],
@@ -276,8 +277,15 @@ def add_adapters(x, y, adapter_ids, a, b, scales, ranks=None, out=None, stream=N
 
 def adapters_status(stream=None):
     """Synchronize the stream; raise when an add_adapters call on the current
-    device gave up a bounded wait (moe_adapters_status)."""
+    device gave up a bounded wait since this was last asked for this stream
+    (moe_adapters_status)."""
     _check(lib().moe_adapters_status(_stream(stream)))
+
+
+def debug_set_adapter_wait_test(withhold_cta, wait_limit_cycles=0):
+    """Test hook (moe_debug_set_adapter_wait_test): the next launch of the adapters'
+    tcgen05 kernel withholds an arrival; its waits give up after the limit."""
+    _check(lib().moe_debug_set_adapter_wait_test(int(withhold_cta), int(wait_limit_cycles)))
 
 
 def _gate(gate, T, H, dev):

@@ -383,9 +383,10 @@ moe_status moe_add_adapters(const void* x, int64_t ld_x, const void* y, int64_t 
                             moe_stream_t stream);
 
 /* Synchronize the stream; MOE_ERR_TIMEOUT when a moe_add_adapters call on the
- * current device has given up a bounded device-side wait since this was last
- * asked (its outputs are invalid then; moe_block_forward's adapters report to
- * moe_sync_status of their handle). */
+ * current device, on this stream or another, has given up a bounded device-side
+ * wait since this was last asked for this stream (its outputs are invalid then).
+ * Every stream that asks is told.  moe_block_forward's adapters report to
+ * moe_sync_status of their handle. */
 moe_status moe_adapters_status(moe_stream_t stream);
 
 #define MOE_GATE_NONE 0
@@ -496,6 +497,14 @@ moe_status moe_debug_get_act_nvfp4(moe_handle h, void* codes, void* scales, moe_
  * setting applies to one launch and then clears; withhold_cta < 0 clears it.
  * Errors: INVALID_ARG (null handle, negative limit). */
 moe_status moe_debug_set_wait_test(moe_handle h, int32_t withhold_cta, int64_t wait_limit_cycles);
+
+/* The same for the request adapters: the next launch of their tcgen05 kernel from
+ * this host thread (by moe_add_adapters or a handle's block) has CTA
+ * `withhold_cta` keep back an arrival that its cluster waits for, and every wait of
+ * that launch gives up after `wait_limit_cycles` SM clock cycles.  The launch
+ * ends with invalid outputs, which moe_adapters_status or moe_sync_status
+ * reports.  One-shot; withhold_cta < 0 clears it.  Errors: INVALID_ARG. */
+moe_status moe_debug_set_adapter_wait_test(int32_t withhold_cta, int64_t wait_limit_cycles);
 
 /* Profiling aid: when events != NULL, every later call records, on its
  * stream, the events of the slots it has:
