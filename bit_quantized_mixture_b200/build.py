@@ -1,7 +1,7 @@
 """Build the CUDA library libmoe_b200.so in-tree with nvcc for sm_100a, and the
 Python extension _binding.so (csrc/binding.cpp) against it.
 
-    python -m bit_quantized_mixture_b200.build [--force] [--verbose]
+    python -m bit_quantized_mixture_b200.build [--force] [--verbose] [--library-only]
 
 Objects go to bit_quantized_mixture_b200/_build/; the shared library is
 written next to this file so that it travels with the source tree.
@@ -24,6 +24,7 @@ LIB = os.path.join(PKG, "libmoe_b200.so")
 INCLUDE = os.path.join(ROOT, "include")
 BINDING = os.path.join(PKG, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+STAMP = os.path.join(BUILD, "binding.stamp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -66,7 +67,28 @@ def binding_command(target):
     return cmd
 
 
-def build(force: bool = False, verbose: bool = False, extra=None) -> str:
+def binding_missing():
+    """What the extension cannot be compiled without and is not here, or None."""
+    if not shutil.which("g++"):
+        return "g++ was not found"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers were not found"
+    try:
+        import torch
+    except ImportError:
+        return "torch cannot be imported"
+    if not os.path.exists(os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd", "python_variable.h")):
+        return "torch's C++ headers were not found"
+    return None
+
+
+def binding_stamp() -> str:
+    """What the extension is compiled against: it fits this Python and this torch only."""
+    import torch
+    return "\n".join([sys.version, torch.__version__] + binding_command(BINDING)) + "\n"
+
+
+def build(force: bool = False, verbose: bool = False, extra=None, binding: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     hdrs = headers()
@@ -83,7 +105,7 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
 
@@ -93,11 +115,26 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         cmd = [cc] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs + ["-lcudart"]
         run(cmd)
         os.replace(LIB + ".tmp", LIB)
+    if not binding:
+        return LIB
+    # the library is complete by itself: its C callers need nothing of what the
+    # extension is compiled with
+    missing = binding_missing()
+    if missing:
+        print(f"_binding.so is not built: {missing}; the library's C interface does not need it, the Python calls around the experts do",
+              file=sys.stderr, flush=True)
+        return LIB
+    stamp, made = binding_stamp(), None
+    if os.path.exists(STAMP):
+        with open(STAMP) as f:
+            made = f.read()
     # the entry points' declarations and the extension's own source (the library
     # is found by name when it is loaded)
-    if force or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "moe_b200.h"), __file__]):
+    if force or made != stamp or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "moe_b200.h"), __file__]):
         run(binding_command(BINDING + ".tmp"))
         os.replace(BINDING + ".tmp", BINDING)
+        with open(STAMP, "w") as f:
+            f.write(stamp)
     return LIB
 
 
@@ -105,8 +142,9 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--force", action="store_true")
     ap.add_argument("--verbose", action="store_true")
+    ap.add_argument("--library-only", action="store_true", help="the C library without the Python extension")
     ap.add_argument("--ptxas-info", action="store_true", help="print register/smem usage per kernel")
     a = ap.parse_args()
     extra = ["-Xptxas", "-v"] if a.ptxas_info else None
-    print(build(force=a.force or a.ptxas_info, verbose=a.verbose or a.ptxas_info, extra=extra))
+    print(build(force=a.force or a.ptxas_info, verbose=a.verbose or a.ptxas_info, extra=extra, binding=not a.library_only))
     sys.exit(0)
