@@ -100,3 +100,19 @@ def test_both_sides_of_each_token_count_that_changes_the_kernel(T, R, wide):
     ids = torch.randint(-1, n, (T,), generator=g).sort().values.to(torch.int32).to(DEV)
     ranks = torch.randint(1, R + 1, (n,), generator=g).to(torch.int32).to(DEV)
     assert_close(moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"], ranks), d, ids, ranks)
+
+
+@pytest.mark.parametrize("T,K,N,R,n", [(1300, 1032, 1000, 128, 5), (1500, 520, 1000, 96, 40), (1900, 520, 520, 72, 30), (1920, 2048, 512, 128, 1)])
+@pytest.mark.parametrize("order", ["token", "request"])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_few_tiles_in_clusters_of_eight(T, K, N, R, n, order, mixed):
+    """Up to 15 tiles of 128 tokens, each split over eight CTAs (K and N have eight
+    chunks): 16 rows of a tile per CTA."""
+    d = make(T, K, N, R, n, seed=T + R)
+    g = torch.Generator().manual_seed(T)
+    ids = torch.randint(-1, n, (T,), generator=g)
+    if order == "request":
+        ids = ids.sort().values
+    ids = ids.to(torch.int32).to(DEV)
+    ranks = torch.randint(0, R + 1, (n,), generator=g).to(torch.int32).to(DEV) if mixed else None
+    assert_close(moe.add_adapters(d["x"], d["y"], ids, d["a"], d["b"], d["scales"], ranks), d, ids, ranks)

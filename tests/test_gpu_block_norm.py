@@ -169,3 +169,18 @@ def test_vectors_between_an_outputs_rows():
     assert torch.equal(got[0], want[0]) and torch.equal(big[:, :H], want[1]) and torch.equal(big[3, H:], d["pre_weight"])
     with pytest.raises(moe.MoeError):
         moe.block_norm(**{**d, "pre_weight": big[2, 8:8 + H]}, x_out=big[:, :H])
+
+
+@pytest.mark.parametrize("T", [4095, 4096])
+@pytest.mark.parametrize("H", [8, 520, 2048])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("gate,sigmoid", [("none", False), ("channel", True), ("token", True), ("element", False)])
+def test_many_rows(T, H, wide, gate, sigmoid):
+    """From 4096 rows on a thread holds four vectors, so that narrow rows are a warp's
+    or two; in place as well."""
+    d = make(T, H, wide, True, gate, True, seed=T + H)
+    got = moe.block_norm(**d, gate_sigmoid=sigmoid)
+    assert_close(got, d, sigmoid, False)
+    r, y = d["r"].clone(), d["y"].clone()
+    moe.block_norm(**{**d, "r": r, "y": y}, gate_sigmoid=sigmoid, r_out=r, x_out=y)
+    assert torch.equal(r, got[0]) and torch.equal(y, got[1])
