@@ -22,9 +22,10 @@ namespace cg = cooperative_groups;
 // the device alone.  A cluster per token reads each token's whole adapter; tiles
 // share it among the tokens of one request, but go through a tile's adapters one
 // after another.  2048 -> 2048, us, tokens of 64 requests mixed / of 12 requests in
-// order: 128 tokens rank 16, by token 6.4 / 6.4, in tiles of 16 28 / 10; 256 tokens
-// 9.4 / 9.4 and 29 / 9.7; 512 tokens 17 / 17 and 32 / 9.2; rank 64, 128 tokens
-// 21 / 21 and 55 / 15; 256 tokens 38 / 38 and 60 / 15.
+// order: 128 tokens rank 16, by token 6.4 / 6.4, in tiles of 16 33 / 12; 256 tokens
+// 9.4 / 9.8 and 34 / 11; 512 tokens 17 / 17 and 35 / 11; rank 64, 128 tokens 22 / 15
+// and 58 / 16; 256 tokens 40 / 25 and 57 / 16: there tokens of many requests lose 17 us
+// by the rule, tokens in order would lose 9 by the other.
 constexpr int kAdTokenMax = 256, kAdTokenWork = 8192;        // most tokens, most tokens x R, of a cluster per token
 // CTAs per token: rank 16, 1 token 3.8 us with 8, 4.6 with 4, 6.9 with 2; 64 tokens
 // 5.6 / 5.4 / 7.1; 128 tokens 9.8 / 6.4 / 7.6; 256 tokens 18 / 11.4 / 9.4.

@@ -48,11 +48,11 @@ constexpr int kTcRows = 128;
 constexpr int kTcEpiWarps = 8;           // 4 per stream
 constexpr int kTcSmall = 11, kTcCleaner = 13, kTcStore = 14, kTcCleaner1 = 15;     // warps
 constexpr int kTcThreads = 32 * (kTcCleaner1 + 1);
-// Two of everything per chunk: an MMA issuer waits, issues and commits for about
-// 700 cycles per chunk of x, and the epilogue of an output chunk is a chain of
-// about 1270, where a chunk's way from memory takes 700 and 1400.  So two issuers
-// and two epilogue groups take turns by chunk, each with rings and accumulators of its own (a parity wait
-// tells only a slot's next use from the last: whoever waits has to see every use).
+// Two of everything per chunk: an MMA issuer's waits and commits, and an epilogue
+// group's chain from accumulator to store, each take about as long as a chunk's way
+// from memory.  So two issuers and two epilogue groups take turns by chunk, each
+// with rings and accumulators of its own (a parity wait tells only a slot's next use
+// from the last: whoever waits has to see every use).
 constexpr int kTcStreams = 2;
 constexpr int kTcTmemCols = 512;
 constexpr int kTcZCols = 256;            // z: adapters of a pass x streams x rank
@@ -401,15 +401,20 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                     tc_fence_after();
                     const uint64_t bd = ds + (uint64_t)(small.slot * (C::SMALL >> 4));
                     const uint32_t dst = tmem + kTcZCols + 64u * (uint32_t)(w * kTcDBufs + buf);
-                    // (unrolled: rank 64, 16 requests, 8192 tokens 49.7 -> 44.8 us)
+                    // (unrolled, 8192 tokens of 16 requests, rank 64: 49.7 -> 44.8 us; the first
+                    // step by itself, 4096 tokens of 12 requests, rank 16: 25.8 -> 24.4 us)
+                    auto step = [&](int q) {
 #pragma unroll
-                    for (int q = 0; q < 4 * RB; ++q)
-                        if (q < steps) {
+                        for (int h = 0; h < kZParts; ++h)
+                            mma_bf16(dst, dz + (uint64_t)((h * RB + (q >> 2)) * (C::ZBLOCK >> 4) + 2 * (q & 3)),
+                                     bd + (uint64_t)((q >> 2) * (NC * 128 >> 4) + 2 * (q & 3)), ido, h + q > 0 ? 1u : 0u);
+                    };
+                    step(0);
+                    if (steps > 1) {
 #pragma unroll
-                            for (int h = 0; h < kZParts; ++h)
-                                mma_bf16(dst, dz + (uint64_t)((h * RB + (q >> 2)) * (C::ZBLOCK >> 4) + 2 * (q & 3)),
-                                         bd + (uint64_t)((q >> 2) * (NC * 128 >> 4) + 2 * (q & 3)), ido, h + q > 0 ? 1u : 0u);
-                        }
+                        for (int q = 1; q < 4 * RB; ++q)
+                            if (q < steps) step(q);
+                    }
                     mma_commit(&small_empty[w][small.slot]);
                     mma_commit(&d_full[w][buf]);
                 }
@@ -531,44 +536,56 @@ k_adapter_tc(const __grid_constant__ AdapterArgs a, const __grid_constant__ TcMa
                 ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_ready, 0u, &abort_flag, err, 52, limit));
             }
             if (ok) {
-                // this CTA's rows, eight columns of one at a time: summed and scaled in
-                // registers, written when nobody needs the sums any more
+                // this CTA's rows, eight columns of one at a time
                 constexpr int ITEMS = kTcRows * RB * 8 / (kTcEpiWarps * 32);
                 const int items = own_rows * (rows_a / 8), i0 = (int)threadIdx.x - 96;
-                float z[ITEMS][8];
+                auto sum = [&](int i, float (&v)[8]) {
+                    const int rl = i % own_rows, j = i / own_rows, r = crank * own_rows + rl;     // row, eight columns
 #pragma unroll
-                for (int u = 0; u < ITEMS; ++u) {
-                    const int i = i0 + u * kTcEpiWarps * 32, rl = i % own_rows, j = i / own_rows, r = crank * own_rows + rl;     // row, eight columns
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) z[u][q] = 0.0f;
-                    if (i >= items || s_id[r] < 0) continue;
+                    for (int q = 0; q < 8; ++q) v[q] = 0.0f;
+                    if (s_id[r] < 0) return;
                     const int rank = rank_of(s_id[r]);
                     const float scale = s_scale[r];
+#pragma unroll 1
                     for (int q = 0; q < CL; ++q) {
                         const float4 v0 = zp[(q * quads + 2 * j) * own_rows + rl], v1 = zp[(q * quads + 2 * j + 1) * own_rows + rl];
-                        z[u][0] += v0.x; z[u][1] += v0.y; z[u][2] += v0.z; z[u][3] += v0.w;
-                        z[u][4] += v1.x; z[u][5] += v1.y; z[u][6] += v1.z; z[u][7] += v1.w;
+                        v[0] += v0.x; v[1] += v0.y; v[2] += v0.z; v[3] += v0.w;
+                        v[4] += v1.x; v[5] += v1.y; v[6] += v1.z; v[7] += v1.w;
                     }
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) z[u][q] = 8 * j + q < rank ? z[u][q] * scale : 0.0f;
-                }
-                if (C::OFF_Z + rows_a * kTcRows * 4 > C::OFF_OP) {       // the operand takes their place
+                    for (int q = 0; q < 8; ++q) v[q] = 8 * j + q < rank ? v[q] * scale : 0.0f;
+                };
+                auto put = [&](int i, const float (&v)[8]) {
+                    const int j = i / own_rows, r = crank * own_rows + i % own_rows;
+                    uint32_t w[4][kZParts];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) split_z2(v[2 * q], v[2 * q + 1], w[q]);
+                    uint8_t* d = smem + C::OFF_OP + (j >> 3) * C::ZBLOCK + sw_piece(r, j & 7);
+#pragma unroll 1
+                    for (int q = 0; q < CL; ++q)
+#pragma unroll
+                        for (int h = 0; h < kZParts; ++h) st_cluster_v4(d + h * RB * C::ZBLOCK, q, make_uint4(w[0][h], w[1][h], w[2][h], w[3][h]));
+                };
+                if (C::OFF_Z + rows_a * kTcRows * 4 <= C::OFF_OP) {
+#pragma unroll 1
+                    for (int i = i0; i < items; i += kTcEpiWarps * 32) {
+                        float z[8];
+                        sum(i, z);
+                        put(i, z);
+                    }
+                } else {
+                    // the operand takes the sums' place: it is written when nobody
+                    // needs them any more
+                    float z[ITEMS][8];
+#pragma unroll
+                    for (int u = 0; u < ITEMS; ++u)
+                        if (i0 + u * kTcEpiWarps * 32 < items) sum(i0 + u * kTcEpiWarps * 32, z[u]);
                     __syncwarp();
                     if (lane < CL) mbar_arrive_cluster(&z_read, lane);
                     ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_read, 0u, &abort_flag, err, 53, limit));
-                }
 #pragma unroll
-                for (int u = 0; u < ITEMS; ++u) {
-                    const int i = i0 + u * kTcEpiWarps * 32, j = i / own_rows, r = crank * own_rows + i % own_rows;
-                    if (!ok || i >= items) continue;
-                    uint32_t w[4][kZParts];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) split_z2(z[u][2 * q], z[u][2 * q + 1], w[q]);
-#pragma unroll
-                    for (int h = 0; h < kZParts; ++h) {
-                        uint8_t* d = smem + C::OFF_OP + (h * RB + (j >> 3)) * C::ZBLOCK + sw_piece(r, j & 7);
-                        for (int q = 0; q < CL; ++q) st_cluster_v4(d, q, make_uint4(w[0][h], w[1][h], w[2][h], w[3][h]));
-                    }
+                    for (int u = 0; u < ITEMS; ++u)
+                        if (ok && i0 + u * kTcEpiWarps * 32 < items) put(i0 + u * kTcEpiWarps * 32, z[u]);
                 }
             }
             if (ok) {

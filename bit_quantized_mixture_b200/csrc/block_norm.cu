@@ -58,6 +58,11 @@ MOE_DEV uint4 pack8(const f32x2 (&v)[4]) {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// The fast exponential and division: a gate is off by up to 2 + 1.2 |g| units of 2^-23
+// of its value (3.3e-6 for |g| up to 65 against 1.9e-7 by expf and a rounded
+// division, which take the row's time past the memory's: 4096 x 8192, fp32 residual,
+// sigmoid of a channel gate 70 against 89 us, 8192 x 2048, of an element gate 29
+// against 42).
 MOE_DEV float gate_of(float g, bool sigmoid) { return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g)) : g; }
 
 // sum over the CTA; buf: one float per warp (zeros behind them up to a multiple

@@ -11,9 +11,9 @@
 // The order is that of the keys in fp64.  Scores rise with their logits, so where
 // two keys are equal there (saturated scores, scores far below their biases) the
 // logits tell the rest: a bias of one value for all experts changes no order.  fp32
-// keys alone would swap about one
-// token's experts in a few thousand, and fp64 keys for every expert bind the
-// kernel to the fp64 exponentials (123 us for 8192 tokens of 512 experts).  So
+// keys alone would swap about one token's experts in a few thousand, and fp64 keys
+// for every expert bind the kernel to the fp64 exponentials (123 us for 8192 tokens
+// of 512 experts).  So
 // select_fast works in fp32 with a bound on each key's error.  Where the last
 // group that stays and the first that does not, or two of the chosen keys, are
 // nearer than their bounds, group_rank_exact and rank_exact take the keys that
@@ -54,8 +54,8 @@ MOE_DEV float warp_max1(float v) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-// exp by the approximate power of two, with __expf's error; results below 2^-126 are
-// 0 (__expf keeps them, for three more instructions): within the bounds below
+// exp(v) = 2^(v log2 e) by the instruction's approximate power of two: off by at most
+// 2 + 1.173 |v| ulp; results below 2^-126 are 0, which is within the bounds below
 MOE_DEV float exp_approx(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
@@ -534,6 +534,9 @@ MOE_DEV bool select_fast(const SelectArgs& a, int t, SelScratch& sc, float* gkey
     for (int i = 0; i < SLOTS; ++i) v[i] = fminf(fmaxf(v[i], -FLT_MAX), FLT_MAX);      // NaN and -inf are off, +inf is capped
     const bool top2 = a.G > 1 && a.top2 && a.per > 1;
     const bool scored = a.bias != nullptr || top2;   // keys or group scores need the scores
+    // (total also divides unnormalised weights: with expf in place of exp_approx their
+    // error over 2000 rows of 600 was 5.8e-8 in place of 6.1e-8 on average and the same
+    // at most, for 8192 rows in 37.5 us in place of 36.2)
     float top = -FLT_MAX, total = 1.0f, ks = 1e-6f;
     if (!a.sigmoid && (scored || !a.renorm)) {
         float s = 0.0f;

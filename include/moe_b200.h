@@ -400,7 +400,8 @@ moe_status moe_adapters_status(moe_stream_t stream);
  *   r' = residual_scale * r + branch_scale * g * u       (no y: the first term)
  *   x  = r' * rsqrt(mean(r'^2) + eps) * (w_pre + o), from r' before its
  *        rounding; o = 1 with unit_offset, else 0
- * in fp32 (a row's squares must not overflow it); r' and x are rounded once. */
+ * in fp32 (a row's squares must not overflow it; a gate's sigmoid to 2 + 1.2 |gate|
+ * units of 2^-23 of its value); r' and x are rounded once. */
 typedef struct {
     const void* r;             /* bf16 or (r_fp32) fp32 [T, H] */
     const void* y;             /* bf16 [T, H] or NULL */
