@@ -31,15 +31,17 @@ constexpr int kAdTokenMax = 256, kAdTokenWork = 8192;        // most tokens, mos
 // 5.6 / 5.4 / 7.1; 128 tokens 9.8 / 6.4 / 7.6; 256 tokens 18 / 11.4 / 9.4.
 constexpr int kAdCluster8 = 32, kAdCluster4 = 192;           // up to so many tokens 8, 4 CTAs
 // 2048 -> 2048, 12 requests in order, us, tiles of 16 tokens / of 128 on tcgen05
-// (adapters_tc.cu), bf16: rank 16, 2800 tokens 22.3 / 24.1, 3700 tokens 29.5 / 28.1, 8192
-// tokens 58 / 35; rank 64, 2500 tokens 31.2 / 33.2, 2800 tokens 34 / 31.4, 8192 tokens
-// 82 / 44; rank 128, 1000 tokens 33 / 42, 1300 tokens 42.3 / 41.7, 8192 tokens 200 / 82.
-// fp32 outputs, tiles of 16 / of 64 / tcgen05: rank 16, 3700 tokens 33 / 36 / 38, 4500
-// tokens 37 / 32 / 49, 6000 tokens 49 / 49 / 51, 8192 tokens 65 / 55 / 48; rank 64, 4500
-// tokens 51 / 52 / 62, 6000 tokens 67 / 77 / 58, 8192 tokens 88 / 83 / 60; rank 128
+// (adapters_tc.cu), bf16: rank 16, 2500 tokens 20.4 / 23.2, 2800 tokens 22.3 / 21.9, 8192
+// tokens 58 / 34; rank 32, 3200 tokens 25.6 / 26.7, 3700 tokens 30.8 / 30.3, 8192 tokens
+// 60 / 36; rank 64, 2500 tokens 31.2 / 33.5, 2800 tokens 34 / 31.7, 8192 tokens 82 / 45;
+// rank 128, 1300 tokens 42 / 44, 1600 tokens 53 / 41, 8192 tokens 200 / 78.  fp32
+// outputs, tiles of 16 / of 64 / tcgen05: rank 16, 3700 tokens 33 / 36 / 31, 4500
+// tokens 37 / 32 / 39, 6000 tokens 49 / 49 / 41, 8192 tokens 65 / 55 / 42; rank 32, 3700
+// tokens 35 / 37 / 41, 6000 tokens 50 / 50 / 54, 8192 tokens 66 / 56 / 51; rank 64, 4500
+// tokens 51 / 52 / 63, 6000 tokens 67 / 77 / 59, 8192 tokens 88 / 83 / 61; rank 128
 // (no tcgen05), 3200 tokens 90 / 94, 3700 tokens 102 / 87, 8192 tokens 202 / 152.
-constexpr int kAdTc32 = 3200, kAdTc64 = 2700, kAdTc128 = 1300;   // from so many tokens on tcgen05: ranks to 32, 64, 128
-constexpr int kAdTcWide32 = 7000, kAdTcWide64 = 5000;            // fp32, likewise
+constexpr int kAdTc16 = 2800, kAdTc32 = 3500, kAdTc64 = 2700, kAdTc128 = 1400;   // from so many tokens on tcgen05: ranks to 16, 32, 64, 128
+constexpr int kAdTcWide16 = 5000, kAdTcWide32 = 7000, kAdTcWide64 = 5000;        // fp32, likewise
 constexpr int kAdTile64Wide32 = 4000, kAdTile64Wide128 = 3600;   // fp32: from so many on tiles of 64 (ranks 33 to 64: never)
 constexpr int kAdThreads = 256;
 
@@ -519,7 +521,8 @@ cudaError_t launch_add_adapters(const AdapterArgs& a, cudaStream_t st) {
         if (a.T <= kAdCluster8) return launch_tokens<8>(a, st);
         return a.T <= kAdCluster4 ? launch_tokens<4>(a, st) : launch_tokens<2>(a, st);
     }
-    const int tc = a.R <= 32 ? (a.wide ? kAdTcWide32 : kAdTc32) : a.R <= 64 ? (a.wide ? kAdTcWide64 : kAdTc64) : kAdTc128;
+    const int tc = a.R <= 16 ? (a.wide ? kAdTcWide16 : kAdTc16) : a.R <= 32 ? (a.wide ? kAdTcWide32 : kAdTc32)
+                 : a.R <= 64 ? (a.wide ? kAdTcWide64 : kAdTc64) : kAdTc128;
     if (a.T >= tc) {
         const cudaError_t e = launch_add_adapters_tc(a, st);
         if (e != cudaErrorNotSupported) return e;
