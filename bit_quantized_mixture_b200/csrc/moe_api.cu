@@ -1210,9 +1210,12 @@ moe_status moe_block_forward(moe_handle h, const moe_block* b, moe_stream_t stre
             g[2] = {ad->scales, (int64_t)ad->num_adapters * 4};
             g[3] = {ad->ranks, (int64_t)ad->num_adapters * 4};
         }
-    for (const Span& g : given)
+    for (const Span& g : given) {
+        if (&g != given && meet(g, given[0]))                    // r, a result as well
+            return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: a result overlaps an input");
         for (int i = b->w_in ? 0 : 1; i < kOut; ++i)             // (without w_in x is given, too)
             if (meet(g, out[i])) return fail(h, MOE_ERR_INVALID_ARG, "moe_block_forward: a result overlaps an input");
+    }
     moe_norm n{};
     n.r = b->r; n.T = T; n.H = H; n.r_fp32 = b->r_fp32;
     n.ld_r = n.ld_y = n.ld_gate = n.ld_r_out = n.ld_x = H;

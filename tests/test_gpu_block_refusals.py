@@ -32,7 +32,8 @@ def test_results_over_one_another_and_over_what_is_given(layer):  # noqa: F811
              dict(layer_adapters=(one(o["x"], (1, 8, H)), b[:1].contiguous(), s[:1].contiguous(), None)),
              dict(layer_adapters=(a[:1].contiguous(), one(o["y"], (1, H, 8)), s[:1].contiguous(), None)),
              dict(layer_adapters=(a, b, f32(o["w"], 3), None)), dict(layer_adapters=(a, b, s, i32(o["logits"], 3))),
-             dict(router_adapters=(a, one(o["x_next"], (3, E, 8)), s, None))]
+             dict(router_adapters=(a, one(o["x_next"], (3, E, 8)), s, None)),
+             dict(w_in=d["r"].view(torch.bfloat16).view(-1)[:H]), dict(adapter_ids=i32(d["r"], T)), dict(layer_adapters=(a, b, f32(d["r"], 3), None))]
     r0 = d["r"].clone()
     for over in cases:
         with pytest.raises(moe.MoeError) as e:
