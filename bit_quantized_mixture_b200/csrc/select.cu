@@ -134,6 +134,10 @@ __device__ __noinline__ double exact_score(const SelectArgs& a, double x, float 
     return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / total;
 }
 
+// A group's score by its two largest keys.  Scores and biases are added apart: the
+// same two scores and biases in another combination, an exact tie, give the same bits.
+MOE_DEV double sum_of_two(double s1, double s2, float b1, float b2) { return (s1 + s2) + ((double)b1 + (double)b2); }
+
 // The whole rule for one token in fp64, one warp, expert e in lane e % 32.
 template <int SLOTS>
 __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
@@ -180,6 +184,7 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
         for (int g = 0; g < a.G; ++g) {
             double b1 = -INFINITY, b2 = -INFINITY;
             float bl = -INFINITY;
+            int e1 = 0, e2 = 0;
 #pragma unroll 1
             for (int i = 0; i < SLOTS; ++i) {
                 const int e = lane + 32 * i;
@@ -187,8 +192,8 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
                     const double v = scored_groups && !a.bias ? score(key[i]) : key[i];
                     const float l = sel_cap(__ldg(row + e));
                     bl = v > b1 || (v == b1 && l > bl) ? l : bl;
-                    if (v > b1) { b2 = b1; b1 = v; }
-                    else if (v > b2) b2 = v;
+                    if (v > b1) { b2 = b1; e2 = e1; b1 = v; e1 = e; }
+                    else if (v > b2) { b2 = v; e2 = e; }
                 }
             }
             const double m1 = warp_max_d(b1);
@@ -196,8 +201,14 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
             if (scored_groups) {
                 // the second largest: the first lane holding the largest offers its next one
                 const int who = __ffs(__ballot_sync(0xffffffffu, b1 == m1)) - 1;
-                const double m2 = warp_max_d(lane == who ? b2 : b1);
-                v = m2 > -INFINITY ? m1 + m2 : m1;
+                const double next = lane == who ? b2 : b1;
+                const double m2 = warp_max_d(next);
+                if (m2 > -INFINITY) {
+                    const int other = __ffs(__ballot_sync(0xffffffffu, next == m2)) - 1;
+                    const int f1 = __shfl_sync(0xffffffffu, e1, who), f2 = __shfl_sync(0xffffffffu, other == who ? e2 : e1, other);
+                    v = sum_of_two(score((double)sel_cap(__ldg(row + f1))), score((double)sel_cap(__ldg(row + f2))),
+                                   a.bias ? sel_cap(__ldg(a.bias + f1)) : 0.0f, a.bias ? sel_cap(__ldg(a.bias + f2)) : 0.0f);
+                }
             }
             const float ml = scored_groups ? 0.0f : warp_max1(b1 == m1 ? bl : -INFINITY);
             if (lane == g) { mine = v; minel = ml; }
@@ -385,23 +396,27 @@ __device__ __noinline__ int group_rank_exact(const SelectArgs& a, const float* r
     }
     __syncwarp();
     for (int j = lane; j < n; j += 32) {
-        const float l = sel_cap(__ldg(row + sc.expert[j]));
-        sc.exact[j] = exact_score(a, (double)l, top, total) + (a.bias ? (double)sel_cap(__ldg(a.bias + sc.expert[j])) : 0.0);
-        sc.key[j] = top2 ? 1u : sel_key(l);          // decides between equal scores that are single keys
+        const float l = sel_cap(__ldg(row + sc.expert[j])), b = a.bias ? sel_cap(__ldg(a.bias + sc.expert[j])) : 0.0f;
+        // sums of two: score and bias apart; single keys: the key, and the logit that
+        // decides between equal ones
+        const double s = exact_score(a, (double)l, top, total);
+        sc.exact[j] = top2 ? s : s + (double)b;
+        sc.key[j] = top2 ? __float_as_uint(b) : sel_key(l);
     }
     __syncwarp();
     double d1 = -INFINITY, d2 = -INFINITY;
     uint32_t dl = 0u;                                // the largest key's logit
+    int j1 = 0, j2 = 0;
     for (int j = 0; j < n; ++j)
         if (sc.order[j] == g) {
-            const double x = sc.exact[j];
             const uint32_t l = sc.key[j];
-            dl = x > d1 || (x == d1 && l > dl) ? l : dl;
-            d2 = fmax(d2, fmin(d1, x));
-            d1 = fmax(d1, x);
+            const double x = top2 ? sc.exact[j] + (double)__uint_as_float(l) : sc.exact[j];
+            if (!top2) dl = x > d1 || (x == d1 && l > dl) ? l : dl;
+            if (x > d1) { d2 = d1; j2 = j1; d1 = x; j1 = j; }
+            else if (x > d2) { d2 = x; j2 = j; }
         }
+    const double mine = top2 && d2 > -INFINITY ? sum_of_two(sc.exact[j1], sc.exact[j2], __uint_as_float(sc.key[j1]), __uint_as_float(sc.key[j2])) : d1;
     __syncwarp();
-    const double mine = top2 && d2 > -INFINITY ? d1 + d2 : d1;
     int rank = 0;
     for (int q = 0; q < a.G; ++q) {
         const double x = __shfl_sync(all, mine, q << gl);

@@ -330,7 +330,8 @@ moe_status moe_set_expert_table(moe_handle h, const void* const* blocks, moe_str
  * Keys and group scores are compared in 64 bits, not in their fp32 roundings.
  * Where two are equal there, the larger logit goes first (for groups by
  * MOE_GROUP_MAX, that of the largest key; scores rise with their logits), then
- * the lower expert or group. */
+ * the lower expert or group; sums of two keys add scores and biases apart, so
+ * that the same ones in another combination tie. */
 typedef struct {
     int32_t score;             /* MOE_SCORE_* */
     int32_t num_groups;        /* 1 (no groups) .. 32, dividing E */

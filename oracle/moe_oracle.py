@@ -555,8 +555,10 @@ def select_experts(logits, k, score="softmax", bias=None, num_groups=1, top_grou
                 mine = [e for e in on if e // per == g]
                 tie[g] = 0.0
                 if group_score == "top2" and per > 1:
-                    v = sorted(((s[e] if bias is None else key[e]) for e in mine), reverse=True)[:2]
-                    value[g] = sum(v) if v else -np.inf
+                    # scores and biases added apart: the same two of each in another
+                    # combination, an exact tie, give the same sum
+                    v = sorted(mine, key=lambda e: s[e] if bias is None else key[e], reverse=True)[:2]
+                    value[g] = sum(s[e] for e in v) + (0.0 if bias is None else sum(min(float(bias[e]), F32_MAX) for e in v)) if v else -np.inf
                 else:
                     value[g], tie[g] = max(((key[e], x[e]) for e in mine), default=(-np.inf, 0.0))
             kept = sorted(range(num_groups), key=lambda g: (-value[g], -tie[g], g))[:top_groups]

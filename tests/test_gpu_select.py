@@ -9,6 +9,7 @@ import torch
 from bit_quantized_mixture_b200 import moe, synth
 from oracle import moe_oracle as O
 from tests.gpu_util import bf16_tensor
+from tests.test_oracle_block import TIES
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -122,6 +123,21 @@ def test_a_bias_of_one_value_changes_no_order(score, shift, spread, E, G, keep, 
     want, _ = run(L, k, score=score, num_groups=G, top_groups=keep)
     got, _ = run(L, k, bias, score=score, num_groups=G, top_groups=keep)
     assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("score,la,lb,b1,b2", TIES)
+@pytest.mark.parametrize("others", [0, 90])
+def test_groups_of_the_same_scores_and_biases_tie(score, la, lb, b1, b2, others):
+    """The lower group stays, with two more groups' worth of low experts and (more equal
+    keys than a list holds) with groups of 92."""
+    per = 2 + others
+    low = lambda pair: pair + [-30.0] * others
+    L = np.array([low([la, lb]) + low([lb, la]) + [-30.0] * per, low([lb, la]) + low([la, lb]) + [-30.0] * per], dtype=np.float32)
+    bias = np.full(3 * per, -1.0, dtype=np.float32)
+    bias[[0, per]], bias[[1, per + 1]] = b1, b2
+    check(L, 2, bias, score=score, num_groups=3, top_groups=1, group_score="top2")
+    ids, _ = run(L, 2, bias, score=score, num_groups=3, top_groups=1, group_score="top2")
+    assert (np.sort(ids, axis=1) == [0, 1]).all()
 
 
 @pytest.mark.parametrize("E,G,keep", [(48, 1, 1), (48, 4, 2), (600, 24, 5), (1024, 1, 1)])

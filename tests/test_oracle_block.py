@@ -56,6 +56,20 @@ def test_keys_that_are_equal_in_64_bits_go_by_their_logits():
         assert O.select_experts(L, 3, bias=bias)[0].tolist() == [[1, 3, 2], [3, 0, 2]]
 
 
+TIES = [("softmax", 0.5, 1.0, 0.375, 0.0), ("softmax", 1.0, 0.5, 0.125, 0.25), ("softmax", -0.5, 0.25, 0.375, 0.0), ("sigmoid", 1.0, 0.5, 0.375, 0.125),
+        ("sigmoid", 0.5, 3.0, -0.125, 0.125), ("sigmoid", 3.0, 0.5, 0.25, -0.125)]
+
+
+@pytest.mark.parametrize("score,la,lb,b1,b2", TIES)
+def test_groups_of_the_same_scores_and_biases_tie(score, la, lb, b1, b2):
+    """(s_a + b_1) + (s_b + b_2) and (s_b + b_1) + (s_a + b_2) are one sum, which a
+    rounding of each key would tell apart: the lower group stays."""
+    bias = np.array([b1, b2, b1, b2, -1, -1], dtype=np.float32)
+    for L in ([la, lb, lb, la, -3, -4], [lb, la, la, lb, -3, -4]):
+        ids, _ = O.select_experts(np.array([L], dtype=np.float32), 2, score=score, bias=bias, num_groups=3, top_groups=1, group_score="top2")
+        assert sorted(ids[0].tolist()) == [0, 1]
+
+
 def test_a_bias_takes_no_part_in_the_scores():
     """Softmax scores 1/2, 1/4, 1/4; a bias that switches expert 0 off leaves the
     others theirs."""
