@@ -144,7 +144,7 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
     const int lane = threadIdx.x & 31;
     const float* row = a.logits + (size_t)t * a.ld;
     double key[SLOTS];                   // -inf: not eligible
-    float top = -INFINITY;
+    float top = -INFINITY, low = INFINITY;
     bool any = false;
 #pragma unroll 1
     for (int i = 0; i < SLOTS; ++i) {
@@ -155,12 +155,14 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
             if (sel_on(l)) {
                 key[i] = (double)sel_cap(l);
                 top = fmaxf(top, sel_cap(l));
+                low = fminf(low, sel_cap(l));
                 any = true;
             }
         }
     }
     any = __any_sync(0xffffffffu, any);
     top = warp_max1(top);
+    const bool differ = top > -warp_max1(-low);      // not all logits of the row are equal
     double total = 0.0;
     if (!a.sigmoid && any) {
 #pragma unroll 1
@@ -181,38 +183,41 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
         // lane g: group g's score, and the logit of its largest key
         double mine = -INFINITY;
         float minel = -INFINITY;
+        int first = 0, second = -1;      // its two experts, where their sum is the score
         for (int g = 0; g < a.G; ++g) {
             double b1 = -INFINITY, b2 = -INFINITY;
             float bl = -INFINITY;
             int e1 = 0, e2 = 0;
+            const int lo = g * a.per, hi = lo + a.per;       // its experts (hi <= E)
 #pragma unroll 1
-            for (int i = 0; i < SLOTS; ++i) {
+            for (int i = lo >> 5; i <= (hi - 1) >> 5; ++i) {
                 const int e = lane + 32 * i;
-                if (e < a.E && e / a.per == g && key[i] > -INFINITY) {
+                if (e >= lo && e < hi && key[i] > -INFINITY) {
                     const double v = scored_groups && !a.bias ? score(key[i]) : key[i];
-                    const float l = sel_cap(__ldg(row + e));
-                    bl = v > b1 || (v == b1 && l > bl) ? l : bl;
+                    if (!scored_groups && v >= b1) {
+                        const float l = sel_cap(__ldg(row + e));
+                        bl = v > b1 ? l : fmaxf(bl, l);
+                    }
                     if (v > b1) { b2 = b1; e2 = e1; b1 = v; e1 = e; }
                     else if (v > b2) { b2 = v; e2 = e; }
                 }
             }
             const double m1 = warp_max_d(b1);
-            double v = m1;
             if (scored_groups) {
                 // the second largest: the first lane holding the largest offers its next one
                 const int who = __ffs(__ballot_sync(0xffffffffu, b1 == m1)) - 1;
                 const double next = lane == who ? b2 : b1;
                 const double m2 = warp_max_d(next);
-                if (m2 > -INFINITY) {
-                    const int other = __ffs(__ballot_sync(0xffffffffu, next == m2)) - 1;
-                    const int f1 = __shfl_sync(0xffffffffu, e1, who), f2 = __shfl_sync(0xffffffffu, other == who ? e2 : e1, other);
-                    v = sum_of_two(score((double)sel_cap(__ldg(row + f1))), score((double)sel_cap(__ldg(row + f2))),
-                                   a.bias ? sel_cap(__ldg(a.bias + f1)) : 0.0f, a.bias ? sel_cap(__ldg(a.bias + f2)) : 0.0f);
-                }
+                const int other = __ffs(__ballot_sync(0xffffffffu, next == m2)) - 1;
+                const int f1 = __shfl_sync(0xffffffffu, e1, who), f2 = __shfl_sync(0xffffffffu, other == who ? e2 : e1, other);
+                if (lane == g) { first = f1; second = m2 > -INFINITY ? f2 : -1; }
             }
             const float ml = scored_groups ? 0.0f : warp_max1(b1 == m1 ? bl : -INFINITY);
-            if (lane == g) { mine = v; minel = ml; }
+            if (lane == g) { mine = m1; minel = ml; }
         }
+        if (second >= 0)
+            mine = sum_of_two(score((double)sel_cap(__ldg(row + first))), score((double)sel_cap(__ldg(row + second))),
+                              a.bias ? sel_cap(__ldg(a.bias + first)) : 0.0f, a.bias ? sel_cap(__ldg(a.bias + second)) : 0.0f);
         int rank = 0;
         for (int g = 0; g < a.G; ++g) {
             const double v = __shfl_sync(0xffffffffu, mine, g);
@@ -232,21 +237,34 @@ __device__ __noinline__ void select_exact(const SelectArgs& a, int t) {
     int my_id = 0;
     bool my_on = false;
     for (int j = 0; j < a.k; ++j) {
-        // the largest key, of those the largest logit (slots that are off: none), of
-        // those the lowest expert
+        // the largest key, the lowest expert on equal ones
         double best = -INFINITY;
-        float bl = -INFINITY;
         int slot = -1;
-#pragma unroll 1
-        for (int i = 0; i < SLOTS; ++i)
-            if ((live >> i) & 1u) {
-                const float l = key[i] > -INFINITY ? sel_cap(__ldg(row + lane + 32 * i)) : -INFINITY;
-                if (slot < 0 || key[i] > best || (key[i] == best && l > bl)) { best = key[i]; bl = l; slot = i; }
-            }
+        bool again = false;              // another of this lane's keys equals its best
+#pragma unroll 4
+        for (int i = 0; i < SLOTS; ++i) {
+            const double v = key[i];
+            const bool on = (live >> i) & 1u, up = on && (slot < 0 || v > best);
+            again = !up && (again || (on && v == best));
+            best = up ? v : best;
+            slot = up ? i : slot;
+        }
         const double m = warp_max_d(slot >= 0 ? best : -INFINITY);
-        const bool top_key = slot >= 0 && best == m;
-        const float ml = warp_max1(top_key ? bl : -INFINITY);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, top_key && bl == ml ? (uint32_t)(lane + 32 * slot) : 0xffffffffu);
+        bool first = slot >= 0 && best == m;
+        const unsigned lanes = __ballot_sync(0xffffffffu, first), twice = __ballot_sync(0xffffffffu, first && again);
+        if (a.bias && differ && m > -INFINITY && (twice || (lanes & (lanes - 1)))) {
+            // ... of equal keys with a bias the largest logit, then the lowest expert
+            float l = -INFINITY;
+#pragma unroll 4
+            for (int i = 0; i < SLOTS; ++i) {
+                const float x = first && ((live >> i) & 1u) && key[i] == m ? sel_cap(__ldg(row + lane + 32 * i)) : -INFINITY;
+                slot = x > l ? i : slot;
+                l = fmaxf(l, x);
+            }
+            const float ml = warp_max1(l);           // (every lane comes here)
+            first = first && l == ml;
+        }
+        const uint32_t e = __reduce_min_sync(0xffffffffu, first ? (uint32_t)(lane + 32 * slot) : 0xffffffffu);
         if ((int)(e & 31u) == lane) live &= ~(1u << (e >> 5));
         if (lane == j) { my_id = (int)e; my_on = m > -INFINITY; }
     }
